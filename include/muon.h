@@ -91,6 +91,7 @@ extern "C" {
 #define MUON_ERR_TIMEOUT (-5)     /* a bounded device-side wait ran out */
 #define MUON_ERR_NONFINITE (-6)   /* ||U||_F was not finite for some matrix */
 #define MUON_ERR_GUARD     (-7)   /* debug canary mode: a workspace guard was overwritten */
+#define MUON_ERR_INDEX     (-8)   /* a token or target was outside the vocabulary */
 
 /* mode bits of muon_orthogonalize and muon_config.mode */
 #define MUON_NS_STANDARD 0  /* A = X X^T, B = bA + cA^2, X <- aX + BX          */
@@ -102,6 +103,10 @@ extern "C" {
 /* element types */
 #define MUON_DTYPE_BF16 0
 #define MUON_DTYPE_F32 1
+
+/* token and target types */
+#define MUON_INDEX_I32 0
+#define MUON_INDEX_I64 1
 
 #define MUON_MAX_STEPS 16
 
@@ -150,9 +155,13 @@ MUON_API int muon_release_workspace(void);
 /*
  * Synchronise the bound stream, then read and clear the device status word.
  * Returns MUON_OK, MUON_ERR_TIMEOUT (a kernel's bounded wait ran out; its
- * outputs are undefined) or MUON_ERR_NONFINITE (a matrix had a non-finite
- * Frobenius norm; that matrix's outputs were left untouched).  If bad_index
- * is not NULL it receives the index of the first non-finite matrix (or -1).
+ * outputs are undefined), MUON_ERR_NONFINITE (a matrix had a non-finite
+ * Frobenius norm; that matrix's outputs were left untouched) or
+ * MUON_ERR_INDEX (a token or target outside the vocabulary, see the lane's
+ * layers).  If bad_index is not NULL it receives the index of the first
+ * non-finite matrix, for MUON_ERR_INDEX the first position of a bad token or
+ * target, or -1.  Of several conditions the first of GUARD, TIMEOUT,
+ * NONFINITE and INDEX is returned; all are cleared.
  */
 MUON_API int muon_device_status(int* bad_index);
 
@@ -365,6 +374,115 @@ MUON_API int muon_clear_shape_coeffs(void);
 #define MUON_NOALLOC_MAX_MATRICES 1024
 #define MUON_NOALLOC_MAX_CHUNKS 65536 /* chunks of 8192 elements: 512 Mi elements in one call */
 MUON_API int muon_normalize_noalloc(int batch, int m, int n, const void* X, void* Y, int dtype, float eps);
+
+/* ---- layers whose parameters the AdamW lane steps ---------------------------
+ *
+ * [NanoGPT-Muon] "从 SGD 到 Muon" gives the embedding, the output head and the
+ * 1-D parameters to AdamW.  These calls are those parameters' own layers --
+ * token embedding, LayerNorm, output head with its loss -- and the gradients
+ * that muon_adamw_step and muon_hybrid_step read.
+ *
+ * Conventions
+ *  - Device pointers, row-major; `ld` is a row stride in elements.  Activations
+ *    and gradients are MUON_DTYPE_BF16 or MUON_DTYPE_F32 as each call says;
+ *    tokens and targets MUON_INDEX_I32 or MUON_INDEX_I64.  The installed config
+ *    is not read.
+ *  - Work is enqueued on the bound stream, which must belong to the current
+ *    device, as must every pointer.  Sums and statistics are fp32 and each
+ *    output is rounded once.  Results repeat bit for bit.
+ *  - `workspace` is the caller's: 256-byte aligned, at least the bytes that the
+ *    matching *_workspace function returns (host only; < 0 on an argument
+ *    error), with any contents, used until the call's work has ended.  Calls
+ *    may be captured into a CUDA graph; graphs and streams that may run at the
+ *    same time need workspaces of their own.  The first call on a device
+ *    allocates the status word and is refused under capture.
+ *  - A token or target outside the vocabulary is found by the kernels:
+ *    muon_device_status returns MUON_ERR_INDEX.  The forward output of such a
+ *    row is NaN; it takes no part in any gradient.
+ *  - Outputs must not overlap inputs, the workspace or each other.
+ *  - Sizes: count, rows, tokens 0 .. 2^31 - 1025, vocab 1 .. 2^31 - 1025, dim
+ *    1 .. 2^20; a call with no rows only writes zeros to the parameter
+ *    gradients.  Errors: MUON_ERR_INVALID_ARG, MUON_ERR_UNSUPPORTED (types),
+ *    nothing enqueued.
+ *  - These launches count in muon_launch_count; muon_profile_* do not time them.
+ */
+
+/*
+ * muon_embedding -- out[t] = scale * table[tokens[t]], fp32 product, rounded
+ * once to out_dtype.  table vocab x dim, out count x dim, both contiguous.
+ * Any alignment: 16-byte aligned pointers and dim % 8 == 0 take 8-element
+ * accesses.
+ */
+MUON_API int muon_embedding(const void* tokens, int token_dtype, long long count, const void* table, int table_dtype,
+                            long long vocab, long long dim, float scale, void* out, int out_dtype);
+
+/*
+ * muon_embedding_backward -- the table's gradient:
+ *     dtable[v] = scale * sum of grad_out[t] over the t with tokens[t] = v,
+ * zero for v = padding_token (-1: none) and for tokens that do not occur; the
+ * whole vocab x dim table is written.  Tokens are sorted and each row's sum
+ * has a fixed order (no atomic adds).  grad_out: count rows, row stride
+ * ld_grad >= dim.
+ */
+MUON_API long long muon_embedding_backward_workspace(long long count, long long vocab, long long dim);
+MUON_API int muon_embedding_backward(const void* tokens, int token_dtype, long long count, const void* grad_out,
+                                     int grad_dtype, long long ld_grad, long long vocab, long long dim, float scale,
+                                     long long padding_token, void* dtable, int dtable_dtype, void* workspace,
+                                     long long workspace_bytes);
+
+/*
+ * muon_layer_norm -- over the last dimension of rows x dim:
+ *     y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps),
+ * var the mean of (x - mean)^2.  y (contiguous) has x's type; mean and rstd
+ * (fp32, one per row) are what the backward pass needs.  weight and bias have
+ * param_dtype; either may be NULL (1 and 0).  ld_x >= dim.
+ */
+MUON_API int muon_layer_norm(const void* x, int x_dtype, long long ld_x, long long rows, long long dim,
+                             const void* weight, const void* bias, int param_dtype, float eps, void* y, float* mean,
+                             float* rstd);
+
+/*
+ * muon_layer_norm_backward -- with xh = (x - mean) rstd and q = grad_out * weight:
+ *     dx = rstd (q - mean(q) - xh mean(q xh)),
+ *     dweight = sum over rows of grad_out * xh,  dbias = sum of grad_out.
+ * grad_out, x and dx (contiguous) have x_dtype; dweight and dbias have
+ * param_dtype, either may be NULL (not computed).
+ */
+MUON_API long long muon_layer_norm_backward_workspace(long long rows, long long dim);
+MUON_API int muon_layer_norm_backward(const void* grad_out, long long ld_grad, const void* x, int x_dtype,
+                                      long long ld_x, long long rows, long long dim, const float* mean,
+                                      const float* rstd, const void* weight, int param_dtype, void* dx, void* dweight,
+                                      void* dbias, void* workspace, long long workspace_bytes);
+
+/*
+ * muon_head_loss -- softmax cross entropy of the output head, per token:
+ *     l = hidden . weight^T,  lse = log sum exp l,  loss = lse - l[target],
+ * without keeping the logits.  hidden: tokens rows of dim bf16, row stride
+ * ld_hidden (a multiple of 8); weight: vocab x dim bf16, contiguous; both
+ * 16-byte aligned, dim % 8 == 0.  Products are exact, sums fp32.  loss and lse
+ * are fp32, one per token; tokens whose target is ignore_index get 0 in both,
+ * cost nothing in the products, and their hidden rows may hold anything.
+ */
+MUON_API long long muon_head_loss_workspace(long long tokens, long long vocab, long long dim, int backward);
+MUON_API int muon_head_loss(const void* hidden, long long ld_hidden, const void* weight, const void* targets,
+                            int target_dtype, long long tokens, long long vocab, long long dim, long long ignore_index,
+                            float* loss, float* lse, void* workspace, long long workspace_bytes);
+
+/*
+ * muon_head_loss_backward -- with p = dloss (softmax(l) - onehot(target)):
+ *     dhidden = p weight,  dweight = p^T hidden,
+ * both bf16, contiguous and 16-byte aligned; either may be NULL (not
+ * computed).  lse is the forward call's; dloss (fp32, one per
+ * token) is the gradient of the per-token loss.  p is rounded to bf16 for the
+ * two products (as the tensor cores take it), whose sums are fp32.  The
+ * vocabulary is walked in pieces whose p fits in 256 MiB (one 256-column tile
+ * at least).  dhidden is 0 for ignored tokens, and so is their share of
+ * dweight whatever their dloss and hidden rows hold.
+ */
+MUON_API int muon_head_loss_backward(const void* hidden, long long ld_hidden, const void* weight, const void* targets,
+                                     int target_dtype, long long tokens, long long vocab, long long dim,
+                                     long long ignore_index, const float* lse, const float* dloss, void* dhidden,
+                                     void* dweight, void* workspace, long long workspace_bytes);
 
 /* ---- tracing ------------------------------------------------------------ */
 

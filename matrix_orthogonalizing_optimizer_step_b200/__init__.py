@@ -12,9 +12,10 @@ import ctypes
 
 from . import _lib
 from ._lib import (  # noqa: F401
-    MUON_DTYPE_BF16, MUON_DTYPE_F32, MUON_ERR_CUDA, MUON_ERR_GUARD, MUON_ERR_INVALID_ARG,
+    MUON_DTYPE_BF16, MUON_DTYPE_F32, MUON_ERR_CUDA, MUON_ERR_GUARD, MUON_ERR_INDEX, MUON_ERR_INVALID_ARG,
     MUON_ERR_NO_MEMORY, MUON_ERR_NONFINITE, MUON_ERR_TIMEOUT,
-    MUON_ERR_UNSUPPORTED, MUON_MAX_SHAPE_SCHEDULES, MUON_MAX_STEPS, MUON_NS_AUTO, MUON_NS_GRAM,
+    MUON_ERR_UNSUPPORTED, MUON_INDEX_I32, MUON_INDEX_I64, MUON_MAX_SHAPE_SCHEDULES, MUON_MAX_STEPS,
+    MUON_NS_AUTO, MUON_NS_GRAM,
     MUON_NS_STANDARD, MUON_OK, MUON_PREC_FP32, STATUS_NAMES,
 )
 
@@ -334,3 +335,9 @@ def muon_launch_count():
 
 def muon_version():
     return int(lib().muon_version())
+
+
+from ._lane import (  # noqa: E402,F401
+    muon_embedding, muon_embedding_backward, muon_head_loss, muon_head_loss_backward, muon_layer_norm,
+    muon_layer_norm_backward,
+)

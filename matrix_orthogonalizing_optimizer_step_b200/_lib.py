@@ -15,6 +15,7 @@ MUON_ERR_NO_MEMORY = -4
 MUON_ERR_TIMEOUT = -5
 MUON_ERR_NONFINITE = -6
 MUON_ERR_GUARD = -7
+MUON_ERR_INDEX = -8
 
 MUON_NS_STANDARD = 0
 MUON_NS_GRAM = 1
@@ -24,6 +25,9 @@ MUON_PREC_FP32 = 0x100
 MUON_DTYPE_BF16 = 0
 MUON_DTYPE_F32 = 1
 
+MUON_INDEX_I32 = 0
+MUON_INDEX_I64 = 1
+
 MUON_MAX_STEPS = 16
 MUON_MAX_SHAPE_SCHEDULES = 64
 
@@ -32,6 +36,7 @@ STATUS_NAMES = {
     MUON_ERR_UNSUPPORTED: "MUON_ERR_UNSUPPORTED", MUON_ERR_CUDA: "MUON_ERR_CUDA",
     MUON_ERR_NO_MEMORY: "MUON_ERR_NO_MEMORY", MUON_ERR_TIMEOUT: "MUON_ERR_TIMEOUT",
     MUON_ERR_NONFINITE: "MUON_ERR_NONFINITE", MUON_ERR_GUARD: "MUON_ERR_GUARD",
+    MUON_ERR_INDEX: "MUON_ERR_INDEX",
 }
 
 # every symbol include/muon.h declares
@@ -43,6 +48,9 @@ EXPORTS = (
     "muon_launch_count", "muon_normalize_noalloc", "muon_adamw_step",
     "muon_set_shape_coeffs", "muon_get_shape_coeffs", "muon_clear_shape_coeffs",
     "muon_hybrid_step", "muon_step_offload", "muon_offload_chunks", "muon_debug_corrupt_guard",
+    "muon_embedding", "muon_embedding_backward", "muon_embedding_backward_workspace",
+    "muon_layer_norm", "muon_layer_norm_backward", "muon_layer_norm_backward_workspace",
+    "muon_head_loss", "muon_head_loss_backward", "muon_head_loss_workspace",
 )
 
 
@@ -101,7 +109,7 @@ def load(path=LIB_PATH):
             "`python -m matrix_orthogonalizing_optimizer_step_b200.build` "
             "(there is no fallback implementation)")
     lib = ctypes.CDLL(path)
-    c_int, c_float, vp = ctypes.c_int, ctypes.c_float, ctypes.c_void_p
+    c_int, c_float, vp, ll = ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_longlong
     sig = {
         "muon_version": (c_int, []),
         "muon_default_config": (c_int, [ctypes.POINTER(MuonConfig)]),
@@ -135,6 +143,15 @@ def load(path=LIB_PATH):
                                       ctypes.POINTER(c_int), c_int, c_int]),
         "muon_offload_chunks": (c_int, [ctypes.POINTER(ctypes.c_longlong), c_int, c_int, ctypes.POINTER(c_int)]),
         "muon_debug_corrupt_guard": (c_int, [c_int]),
+        "muon_embedding": (c_int, [vp, c_int, ll, vp, c_int, ll, ll, c_float, vp, c_int]),
+        "muon_embedding_backward_workspace": (ll, [ll, ll, ll]),
+        "muon_embedding_backward": (c_int, [vp, c_int, ll, vp, c_int, ll, ll, ll, c_float, ll, vp, c_int, vp, ll]),
+        "muon_layer_norm": (c_int, [vp, c_int, ll, ll, ll, vp, vp, c_int, c_float, vp, vp, vp]),
+        "muon_layer_norm_backward_workspace": (ll, [ll, ll]),
+        "muon_layer_norm_backward": (c_int, [vp, ll, vp, c_int, ll, ll, ll, vp, vp, vp, c_int, vp, vp, vp, vp, ll]),
+        "muon_head_loss_workspace": (ll, [ll, ll, ll, c_int]),
+        "muon_head_loss": (c_int, [vp, ll, vp, vp, c_int, ll, ll, ll, ll, vp, vp, vp, ll]),
+        "muon_head_loss_backward": (c_int, [vp, ll, vp, vp, c_int, ll, ll, ll, ll, vp, vp, vp, vp, vp, ll]),
     }
     assert set(sig) == set(EXPORTS)
     for name, (res, args) in sig.items():

@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "../../include/muon.h"
+#include "lane.h"
 #include "plan.h"
 
 using namespace muon;
@@ -112,6 +113,16 @@ int check_cfg(const muon_config& c) {
     return MUON_OK;
 }
 
+// True while the bound stream is being captured into a CUDA graph.
+bool capturing() {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(g_stream, &st) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return st != cudaStreamCaptureStatusNone;
+}
+
 // Current device's state; allocates the status word on first use.
 int device_state(DeviceState** out) {
     int dev = 0;
@@ -125,6 +136,9 @@ int device_state(DeviceState** out) {
             *out = &d;
             return MUON_OK;
         }
+    if (capturing())
+        return fail(MUON_ERR_UNSUPPORTED,
+                    "the first call on a device allocates its status word: make one call before capturing");
     DeviceState d;
     d.device = dev;
     cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
@@ -134,7 +148,7 @@ int device_state(DeviceState** out) {
         cudaGetLastError();
         return fail(MUON_ERR_NO_MEMORY, "status word allocation failed");
     }
-    const DeviceStatus init{0, 0x7fffffff};
+    const DeviceStatus init{0, kNoBad, kNoBad};
     cudaMemcpy(d.status, &init, sizeof(init), cudaMemcpyHostToDevice);
     if (cudaEventCreateWithFlags(&d.ws_event, cudaEventDisableTiming) != cudaSuccess) {
         cudaGetLastError();
@@ -215,16 +229,6 @@ struct Profiler : ProfileSink {
     }
 };
 Profiler g_prof;
-
-// True while the bound stream is being captured into a CUDA graph.
-bool capturing() {
-    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(g_stream, &st) != cudaSuccess) {
-        cudaGetLastError();
-        return false;
-    }
-    return st != cudaStreamCaptureStatusNone;
-}
 
 // Order this call's use of the workspace after its last use on another stream.
 // Under stream capture the ordering belongs to the capture (it starts after
@@ -508,6 +512,18 @@ int offload_resources(DeviceState* ds, int groups) {
 namespace muon {
 cudaStream_t bound_stream() { return g_stream; }
 void set_last_error(const char* msg) { g_err = msg; }
+
+int abi_fail(int code, const char* msg) { return fail(code, msg); }
+int abi_device(DeviceStatus** status, int* num_sms, int* cc_major) {
+    DeviceState* ds = nullptr;
+    const int st = device_state(&ds);
+    if (st != MUON_OK) return st;
+    *status = ds->status;
+    *num_sms = ds->num_sms;
+    *cc_major = ds->cc_major;
+    return MUON_OK;
+}
+void abi_count_launches(long long n) { g_launches += n; }
 }  // namespace muon
 
 extern "C" {
@@ -577,13 +593,17 @@ int muon_device_status(int* bad_index) {
     DeviceStatus h;
     e = cudaMemcpy(&h, ds->status, sizeof(h), cudaMemcpyDeviceToHost);
     if (e != cudaSuccess) return fail(MUON_ERR_CUDA, std::string("status read failed: ") + cudaGetErrorString(e));
-    const DeviceStatus init{0, 0x7fffffff};
+    const DeviceStatus init{0, kNoBad, kNoBad};
     cudaMemcpy(ds->status, &init, sizeof(init), cudaMemcpyHostToDevice);
-    if (bad_index && h.first_bad != 0x7fffffff) *bad_index = h.first_bad;
+    if (bad_index && h.first_bad != kNoBad) *bad_index = h.first_bad;
     if (h.bits & ST_GUARD)
         return fail(MUON_ERR_GUARD, "a workspace guard was overwritten (a write past the end of a workspace region)");
     if (h.bits & ST_TIMEOUT) return fail(MUON_ERR_TIMEOUT, "a kernel's bounded wait ran out");
     if (h.bits & ST_NONFINITE) return fail(MUON_ERR_NONFINITE, "non-finite Frobenius norm");
+    if (h.bits & ST_INDEX) {
+        if (bad_index) *bad_index = h.first_bad_token;
+        return fail(MUON_ERR_INDEX, "a token or target outside the vocabulary");
+    }
     return MUON_OK;
 }
 

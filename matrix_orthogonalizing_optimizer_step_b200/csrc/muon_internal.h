@@ -10,7 +10,7 @@ enum DType : int { DT_BF16 = 0, DT_F32 = 1, DT_F16 = 2 };
 inline int dtype_size(int dt) { return dt == DT_F32 ? 4 : 2; }
 
 // device status word bits
-enum : int { ST_TIMEOUT = 1, ST_NONFINITE = 2, ST_GUARD = 4 };
+enum : int { ST_TIMEOUT = 1, ST_NONFINITE = 2, ST_GUARD = 4, ST_INDEX = 8 };
 
 // Workspace guards of the debug canary mode (MUON_DEBUG_CANARY=1).
 constexpr int kGuardBytes = 1024;
@@ -19,7 +19,9 @@ constexpr unsigned char kGuardByte = 0xA5;
 struct DeviceStatus {
     int bits;       // ST_* flags, sticky until read by the host
     int first_bad;  // first matrix index with a non-finite norm (or -1 after clear)
+    int first_bad_token;  // first position of a token or target outside the vocabulary
 };
+constexpr int kNoBad = 0x7fffffff;  // first_bad and first_bad_token when there is none
 
 // Fused epilogue of every GEMM:
 //   v = sigma * (alpha * acc + beta * C1) + gamma * C2 + delta * [row == col]

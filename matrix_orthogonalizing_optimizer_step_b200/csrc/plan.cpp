@@ -29,6 +29,7 @@
 #include <tuple>
 
 #include "../../include/muon.h"
+#include "lane.h"
 
 namespace muon {
 namespace {
@@ -101,6 +102,8 @@ bool canary_mode() {
     return v && v[0] == '1';
 }
 
+}  // namespace
+
 // Bound of every device-side wait (MUON_WAIT_LIMIT_MS, 1 ms .. 10 s; default 1 s).
 unsigned long long wait_limit_ns() {
     const char* v = std::getenv("MUON_WAIT_LIMIT_MS");
@@ -108,6 +111,8 @@ unsigned long long wait_limit_ns() {
     ms = std::max(1LL, std::min(ms, 10000LL));
     return static_cast<unsigned long long>(ms) * 1000000ull;
 }
+
+namespace {
 
 bool restart_at(unsigned mask, int k) { return k > 0 && k < 32 && ((mask >> k) & 1u); }
 
