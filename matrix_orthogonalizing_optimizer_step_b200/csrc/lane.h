@@ -70,7 +70,7 @@ struct NormFwd {
     float* mean;
     float* rstd;
 };
-cudaError_t launch_layer_norm(const NormFwd& L, cudaStream_t stream);
+cudaError_t launch_layer_norm(const NormFwd& L, int num_sms, cudaStream_t stream);
 
 struct NormBwd {
     const void* dy;      // row stride ldy

@@ -210,7 +210,7 @@ int muon_layer_norm(const void* x, int x_dtype, long long ld_x, long long rows, 
     L.mean = mean;
     L.rstd = rstd;
     Range r("muon layer norm");
-    return launched(launch_layer_norm(L, bound_stream()), 1);
+    return launched(launch_layer_norm(L, dev.num_sms, bound_stream()), 1);
 }
 
 long long muon_layer_norm_backward_workspace(long long rows, long long dim) {
