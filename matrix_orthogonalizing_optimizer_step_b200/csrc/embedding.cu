@@ -10,19 +10,22 @@
 // The gradient sorts the tokens, so that each table row is summed by whoever
 // owns its run of the sorted order and no atomic add is needed: the order of
 // every sum is fixed by the tokens alone, and results repeat bit for bit.
-//   1. one launch whose first cluster of 8 CTAs sorts (token, position) pairs
-//      (stable radix sort over the bits a token needs) while all other CTAs
-//      write zeros over the table: the zero fill needs no order and is the
-//      longer of the two at every size where either matters;
+//   1. one launch in which one CTA (a cluster of 8 for more tokens than it
+//      holds) sorts (token, position) pairs with a stable radix sort over the
+//      bits a token needs, while all other CTAs write zeros over the table:
+//      the zero fill needs no order and is the longer of the two at every size
+//      where either matters;
 //   2. the sorted order is cut into chunks of kChunk positions; a warp sums
 //      the rows of one chunk for 256 columns.  A token whose run lies inside
 //      a chunk is written at once.  A run that crosses chunk borders leaves
-//      one fp32 partial row per chunk;
-//   3. the partial rows of each crossing run are added in order.
+//      one fp32 partial row per chunk, and its first chunk a note;
+//   3. the partial rows of each noted run are added in order.
 // The cut at fixed positions keeps a frequent token (or a padding token that
 // fills half a batch) from becoming one warp's serial loop.
 //
 // Sums are fp32 and rounded once to the gradient's type.
+#include <algorithm>
+
 #include "lane.h"
 #include "ptx.cuh"
 #include "rows.cuh"
@@ -84,26 +87,200 @@ __global__ void __launch_bounds__(kFwdWarps * 32) embedding_kernel(const EmbedFw
     }
 }
 
+// ---- gradient: order of up to kClassTokens tokens by classes of the vocabulary -----
+
+constexpr int kChunk = 16;                // ordered positions per reduction chunk
+constexpr int kClassTokens = 16384;
+constexpr int kClassRows = 2048;          // table rows of a class at most
+constexpr long long kClassVocab = 1 << 20;
+constexpr int kMostClasses = 148;         // one CTA per SM
+constexpr int kClassThreads = 512;
+constexpr int kClassWarps = kClassThreads / 32;
+constexpr int kPosBits = 14;
+static_assert(kClassTokens <= 1 << kPosBits, "positions of a class's tokens");
+
+struct ClassArgs {
+    const void* tokens;
+    int tokens_i64;
+    int count, vocab, classes;
+    unsigned magic;     // ceil(2^32 / classes): token / classes = umulhi(token, magic), exact for tokens below 2^20
+    long long padding;
+    unsigned* keys;     // tokens in order, `vocab` for those that take no part (last)
+    unsigned* pos;      // their positions
+    unsigned* done;     // counters to zero for the adding launch
+    int ndone;
+    void* out;
+    long long dim;
+    DeviceStatus* status;
+};
+
+// 32-bit words of the list of a class's tokens.
+__host__ __device__ constexpr int class_list_words(int count) {
+    return (count + kClassThreads - 1) / kClassThreads * kClassThreads;
+}
+
+// Zeros over one table row by one warp, 16 bytes a lane from the first aligned address on.
+template <typename TO>
+__device__ __forceinline__ void zero_row(TO* row, long long dim, int lane) {
+    char* p = reinterpret_cast<char*>(row);
+    const long long bytes = dim * sizeof(TO);
+    const long long head = min(static_cast<long long>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15), bytes);
+    const long long n16 = (bytes - head) / 16;
+    uint4* q = reinterpret_cast<uint4*>(p + head);
+    for (long long i = lane; i < n16; i += 32) q[i] = make_uint4(0, 0, 0, 0);
+    if (lane < head) p[lane] = 0;
+    if (lane < bytes - head - n16 * 16) p[head + n16 * 16 + lane] = 0;
+}
+
+// CTA c owns the table rows c, c + classes, c + 2 classes, ...: it finds the
+// tokens of its class among all (each CTA reads all of them, from L2) and
+// groups them by row in the order of their positions.  Then it writes zeros
+// over the rows that no token asks for: a launch of its own, since loads are
+// several times slower while the memory takes writes at its full rate.
+template <typename TO>
+__global__ void __launch_bounds__(kClassThreads) class_group_kernel(const ClassArgs A) {
+    extern __shared__ unsigned class_smem[];
+    __shared__ int count[kClassRows];
+    __shared__ unsigned short start[kClassRows];  // first place of the row's group
+    __shared__ int warp_n[kClassWarps], warp_before[kClassWarps], warp_sum[kClassWarps];
+    unsigned* list = class_smem;  // row << 14 | position: each warp's finds from its first token's place on
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    const int classes = A.classes, cls = blockIdx.x;
+    const int rows = (A.vocab - cls + classes - 1) / classes;
+    for (int r = tid; r < kClassRows; r += kClassThreads) count[r] = 0;
+    for (int i = cls * kClassThreads + tid; i < A.ndone; i += classes * kClassThreads) A.done[i] = 0;
+    __syncthreads();
+    // this warp's stretch of the tokens, 32 at a time
+    const int items = (A.count + kClassThreads - 1) / kClassThreads;
+    const int w0 = warp * items * 32;
+    int found = 0, before = 0;
+    constexpr int kLoads = 8;
+#pragma unroll 1
+    for (int i0 = 0; i0 < items; i0 += kLoads) {
+        long long id[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int t = w0 + (i0 + i) * 32 + lane;
+            id[i] = i0 + i < items && t < A.count ? token_at(A.tokens, A.tokens_i64, t) : A.padding;
+            if (id[i] == A.padding) id[i] = -2;  // takes no part
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int t = w0 + (i0 + i) * 32 + lane;
+            const bool in = i0 + i < items && t < A.count;
+            const bool ok = in && id[i] >= 0 && id[i] < A.vocab;
+            const unsigned q = __umulhi(static_cast<unsigned>(id[i]), A.magic);
+            const int c = static_cast<int>(static_cast<unsigned>(id[i]) - q * classes);
+            const unsigned votes = __ballot_sync(0xffffffffu, ok && c == cls);
+            before += __popc(__ballot_sync(0xffffffffu, ok && c < cls));
+            if (ok && c == cls) {
+                list[w0 + found + __popc(votes & ((1u << lane) - 1))] = q << kPosBits | static_cast<unsigned>(t);
+                atomicAdd(&count[q], 1);
+            }
+            found += __popc(votes);
+            if (cls == 0 && in && !ok) {
+                const long long tok = token_at(A.tokens, A.tokens_i64, t);
+                if (tok < 0 || tok >= A.vocab) report_bad_token(A.status, t);
+            }
+        }
+    }
+    if (lane == 0) {
+        warp_n[warp] = found;
+        warp_before[warp] = before;
+    }
+    __syncthreads();
+    // first place of every row's group: kClassRows / kClassThreads rows per thread
+    {
+        constexpr int kPer = kClassRows / kClassThreads;
+        int n[kPer], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            n[i] = count[tid * kPer + i];
+            mine += n[i];
+        }
+        int scan = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += up;
+        }
+        if (lane == 31) warp_sum[warp] = scan;
+        __syncthreads();
+        int at = scan - mine;
+        for (int w = 0; w < warp; ++w) at += warp_sum[w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            start[tid * kPer + i] = static_cast<unsigned short>(at);
+            at += n[i];
+        }
+    }
+    // the warps' finds as one list, where they are few enough to move
+    int lists = kClassWarps, total = 0, at = 0, most = 0;
+    before = 0;
+    for (int w = 0; w < kClassWarps; ++w) {
+        if (w == warp) at = total;
+        total += warp_n[w];
+        most = max(most, warp_n[w]);
+        before += warp_before[w];
+    }
+    if (most <= 4 * 32) {
+        unsigned e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i * 32 + lane < found) e[i] = list[w0 + i * 32 + lane];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i * 32 + lane < found) list[at + i * 32 + lane] = e[i];
+        lists = 1;
+    }
+    __syncthreads();
+    // one warp groups a row
+    for (int r = warp; r < rows; r += kClassWarps) {
+        const int n = count[r];
+        if (n == 0) continue;
+        const unsigned place = before + start[r];
+        for (int i = lane; i < n; i += 32) A.keys[place + i] = cls + r * classes;
+        int got = 0;
+        for (int w = 0; w < lists && got < n; ++w) {
+            const int k = lists == 1 ? total : warp_n[w];
+            const unsigned* l = list + w * items * 32;
+            for (int i0 = 0; i0 < k && got < n; i0 += 32) {
+                const unsigned e = i0 + lane < k ? l[i0 + lane] : 0;
+                const bool on = i0 + lane < k && (e >> kPosBits) == static_cast<unsigned>(r);
+                const unsigned votes = __ballot_sync(0xffffffffu, on);
+                if (on) A.pos[place + got + __popc(votes & ((1u << lane) - 1))] = e & ((1u << kPosBits) - 1);
+                got += __popc(votes);
+            }
+        }
+    }
+    if (cls == classes - 1)  // tokens that take no part
+        for (int k = before + total + tid; k < A.count; k += kClassThreads) A.keys[k] = A.vocab;
+    for (int r = warp; r < rows; r += kClassWarps)
+        if (count[r] == 0) zero_row(static_cast<TO*>(A.out) + static_cast<long long>(cls + r * classes) * A.dim, A.dim, lane);
+}
+
 // ---- gradient: sort and zero fill -----------------------------------------------
 
 constexpr int kCluster = 8;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMaxBins = 256;
+constexpr int kMaxBits = 9;                           // digit: two passes hold any vocabulary below 2^18
+constexpr int kMaxBins = 1 << kMaxBits;
 constexpr int kItems = 4;                             // pairs per thread and tile
 constexpr int kSortTile = kSortThreads * kItems;      // pairs per CTA and tile
-constexpr int kChunk = 16;                            // sorted positions per reduction chunk
 
 struct SortArgs {
     const void* tokens;
     int tokens_i64;
     unsigned count;
-    unsigned vocab;          // sentinel key: padding and bad tokens sort behind every real one
+    unsigned vocab;          // keys from here on (padding, bad tokens) sort behind every real one
     long long padding;
     unsigned* keys[2];       // ping-pong buffers; the result is in keys[passes & 1], pos[passes & 1]
     unsigned* pos[2];
-    unsigned* counts;        // kCluster x kMaxBins
     int passes, digit_bits;
+    unsigned* done;          // counters to zero for the adding launch
+    long long ndone;
     DeviceStatus* status;
 };
 
@@ -113,27 +290,86 @@ struct FillArgs {
 };
 
 struct SortShared {
-    unsigned warp_hist[kSortWarps][kMaxBins];
-    unsigned base[kMaxBins];   // next output position of each digit for this CTA
-    unsigned scan[kMaxBins];
+    unsigned short warp_hist[kSortWarps][kMaxBins];  // counts, then places within the tile
+    unsigned totals[kCluster][kMaxBins];             // every CTA's digit counts (written by that CTA)
+    unsigned base[kMaxBins];                         // next output position of each digit for this CTA
+    unsigned warp_sum[kSortWarps];
 };
 
-// key of token t in pass 0
+// Key of token t in pass 0: the sentinel `vocab` for padding, vocab + 1 for a
+// token outside the vocabulary (reported once the loads are under way).
 __device__ __forceinline__ unsigned first_key(const SortArgs& S, unsigned t) {
     const long long id = token_at(S.tokens, S.tokens_i64, t);
-    if (id < 0 || id >= S.vocab) {
-        report_bad_token(S.status, t);
-        return S.vocab;
-    }
-    return id == S.padding ? S.vocab : static_cast<unsigned>(id);
+    const unsigned k = id == S.padding ? S.vocab : static_cast<unsigned>(id);
+    return id < 0 || id >= S.vocab ? S.vocab + 1 : k;
 }
 
+// base[d] = `before` + the total of all smaller digits; thread d brings the total of digit d.
+__device__ __forceinline__ void digit_bases(unsigned* base, unsigned* warp_sum, int bins, unsigned total,
+                                            unsigned before) {
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    unsigned scan = total;  // inclusive, within the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned up = __shfl_up_sync(0xffffffffu, scan, o);
+        if (lane >= o) scan += up;
+    }
+    if (lane == 31) warp_sum[warp] = scan;
+    __syncthreads();
+    if (tid < bins) {
+        unsigned below = 0;
+        for (int w = 0; w < warp; ++w) below += warp_sum[w];
+        base[tid] = below + scan - total + before;
+    }
+    __syncthreads();
+}
+
+// Every CTA of the cluster learns this CTA's count of digit `tid`, then
+// base[d] = pairs of smaller digits anywhere + pairs of digit d in earlier CTAs.
+__device__ void sort_bases(SortShared& sh, int bins, int rank, unsigned mine) {
+    const int tid = threadIdx.x;
+    if (tid < bins) {
+        const uint32_t at = smem_u32(&sh.totals[rank][tid]);
+#pragma unroll
+        for (int c = 0; c < kCluster; ++c)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_cta(at, c)), "r"(mine) : "memory");
+    }
+    cluster_sync_all();
+    unsigned total = 0, before = 0;
+    if (tid < bins) {
+#pragma unroll
+        for (int c = 0; c < kCluster; ++c) {
+            const unsigned n = sh.totals[c][tid];
+            if (c < rank) before += n;
+            total += n;
+        }
+    }
+    digit_bases(sh.base, sh.warp_sum, bins, total, before);
+}
+
+// Lanes of the warp that are on and hold the same digit as this one (this
+// lane's own bit included if it is on): one vote per bit of the digit.
+__device__ __forceinline__ unsigned digit_peers(unsigned d, int bits, bool on) {
+    unsigned peers = __ballot_sync(0xffffffffu, on);
+    for (int b = 0; b < bits; ++b) {
+        const bool bit = (d >> b) & 1u;
+        const unsigned votes = __ballot_sync(0xffffffffu, bit);
+        peers &= bit ? votes : ~votes;
+    }
+    return peers;
+}
+
+// Stable radix sort of the pairs (token, position) by the cluster's CTAs, each
+// owning a contiguous stretch.  Within a tile, warp w takes 32 * kItems
+// consecutive pairs; a pair's place is the count of its digit in earlier CTAs,
+// tiles, warps, rows and lanes.  A stretch of one tile (any count up to
+// kCluster * kSortTile) is read once per pass.
 __device__ void sort_cluster(const SortArgs& S, SortShared& sh, int rank) {
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int bins = 1 << S.digit_bits;
-    // CTA `rank` owns a contiguous stretch of the pairs
     const unsigned len = ((S.count + kCluster - 1) / kCluster + 31) / 32 * 32;
     const unsigned lo = min(static_cast<unsigned>(rank) * len, S.count), hi = min(lo + len, S.count);
+    const bool one_tile = len <= kSortTile;
     for (int p = 0; p < S.passes; ++p) {
         const unsigned* kin = S.keys[p & 1];
         const unsigned* pin = S.pos[p & 1];
@@ -142,38 +378,19 @@ __device__ void sort_cluster(const SortArgs& S, SortShared& sh, int rank) {
         const int shift = p * S.digit_bits;
         // earlier passes' pairs come from other CTAs: read at L2
         auto key_of = [&](unsigned i) { return p == 0 ? first_key(S, i) : __ldcg(kin + i); };
-        // digit counts of the whole stretch
-        for (int b = tid; b < kMaxBins; b += kSortThreads) sh.base[b] = 0;
-        __syncthreads();
-        for (unsigned i = lo + tid; i < hi; i += kSortThreads)
-            atomicAdd(&sh.base[(key_of(i) >> shift) & (bins - 1)], 1u);
-        __syncthreads();
-        for (int b = tid; b < bins; b += kSortThreads) S.counts[rank * kMaxBins + b] = sh.base[b];
-        cluster_sync_all();
-        // base[d] = pairs of smaller digits anywhere + pairs of digit d in earlier CTAs
-        unsigned total = 0, before = 0;
-        if (tid < bins) {
-            for (int c = 0; c < kCluster; ++c) {
-                const unsigned n = __ldcg(S.counts + c * kMaxBins + tid);
-                if (c < rank) before += n;
-                total += n;
-            }
-            sh.scan[tid] = total;
+        if (!one_tile) {  // digit counts of the whole stretch first
+            for (int b = tid; b < bins; b += kSortThreads) sh.base[b] = 0;
+            __syncthreads();
+            for (unsigned i = lo + tid; i < hi; i += kSortThreads)
+                atomicAdd(&sh.base[(key_of(i) >> shift) & (bins - 1)], 1u);
+            __syncthreads();
+            const unsigned mine = tid < bins ? sh.base[tid] : 0;
+            sort_bases(sh, bins, rank, mine);
         }
-        __syncthreads();
-        for (int o = 1; o < bins; o <<= 1) {
-            unsigned add = 0;
-            if (tid < bins && tid >= o) add = sh.scan[tid - o];
-            __syncthreads();
-            if (tid < bins) sh.scan[tid] += add;
-            __syncthreads();
-        }
-        if (tid < bins) sh.base[tid] = sh.scan[tid] - total + before;
-        __syncthreads();
-        // stable scatter, one tile at a time: warp w takes 32 * kItems consecutive pairs
-        for (unsigned t0 = lo; t0 < hi; t0 += kSortTile) {
-            for (int b = tid; b < kSortWarps * kMaxBins; b += kSortThreads) (&sh.warp_hist[0][0])[b] = 0;
-            __syncthreads();
+        // (a stretch without pairs still takes part in the exchange)
+        for (unsigned t0 = lo; t0 < hi || (one_tile && t0 == lo); t0 += kSortTile) {
+            uint4* z = reinterpret_cast<uint4*>(&sh.warp_hist[0][0]);
+            for (int b = tid; b < kSortWarps * kMaxBins / 8; b += kSortThreads) z[b] = make_uint4(0, 0, 0, 0);
             unsigned key[kItems], val[kItems], rnk[kItems];
             bool on[kItems];
 #pragma unroll
@@ -183,51 +400,58 @@ __device__ void sort_cluster(const SortArgs& S, SortShared& sh, int rank) {
                 key[r] = on[r] ? key_of(i) : 0;
                 val[r] = on[r] ? (p == 0 ? i : __ldcg(pin + i)) : 0;
             }
+            if (p == 0) {
+#pragma unroll
+                for (int r = 0; r < kItems; ++r)
+                    if (key[r] == S.vocab + 1) report_bad_token(S.status, val[r]);
+            }
+            __syncthreads();
 #pragma unroll
             for (int r = 0; r < kItems; ++r) {
                 const unsigned d = (key[r] >> shift) & (bins - 1);
-                const unsigned peers = __match_any_sync(0xffffffffu, on[r] ? d : kMaxBins + lane);
+                const unsigned peers = digit_peers(d, S.digit_bits, on[r]);
                 rnk[r] = __popc(peers & ((1u << lane) - 1));
                 if (on[r]) rnk[r] += sh.warp_hist[warp][d];
                 __syncwarp();
-                if (on[r] && (peers >> lane) == 1u) sh.warp_hist[warp][d] += __popc(peers);  // the last peer
+                if (on[r] && (peers >> lane) == 1u) sh.warp_hist[warp][d] = rnk[r] + 1;  // the last peer
                 __syncwarp();
             }
             __syncthreads();
+            unsigned tile = 0;
             if (tid < bins) {
-                unsigned run = sh.base[tid];
+                unsigned n[kSortWarps];
+#pragma unroll
+                for (int w = 0; w < kSortWarps; ++w) n[w] = sh.warp_hist[w][tid];
+#pragma unroll
                 for (int w = 0; w < kSortWarps; ++w) {
-                    const unsigned n = sh.warp_hist[w][tid];
-                    sh.warp_hist[w][tid] = run;
-                    run += n;
+                    sh.warp_hist[w][tid] = static_cast<unsigned short>(tile);
+                    tile += n[w];
                 }
-                sh.base[tid] = run;
             }
-            __syncthreads();
+            if (one_tile)
+                sort_bases(sh, bins, rank, tile);
+            else
+                __syncthreads();
 #pragma unroll
             for (int r = 0; r < kItems; ++r) {
                 if (!on[r]) continue;
-                const unsigned at = sh.warp_hist[warp][(key[r] >> shift) & (bins - 1)] + rnk[r];
+                const unsigned d = (key[r] >> shift) & (bins - 1);
+                const unsigned at = sh.base[d] + sh.warp_hist[warp][d] + rnk[r];
                 kout[at] = key[r];
                 pout[at] = val[r];
             }
             __syncthreads();
+            if (tid < bins) sh.base[tid] += tile;
         }
         cluster_sync_all();  // the next pass reads every CTA's output
     }
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
-    sort_and_fill_kernel(const SortArgs S, const FillArgs F) {
-    __shared__ SortShared sh;
-    if (blockIdx.x < kCluster) {
-        sort_cluster(S, sh, static_cast<int>(blockIdx.x));
-        return;
-    }
-    // zeros over the table (the runs' rows are written by the next launch);
-    // every part writes whole 16-byte units from the first aligned address on
-    const long long nthr = static_cast<long long>(gridDim.x - kCluster) * kSortThreads;
-    const long long i0 = static_cast<long long>(blockIdx.x - kCluster) * kSortThreads + threadIdx.x;
+// Zeros over the table (the runs' rows are written by the next launch), by
+// CTA `cta` of `ctas`: whole 16-byte units from the first aligned address on.
+__device__ void fill_zero(const FillArgs& F, int cta, int ctas) {
+    const long long nthr = static_cast<long long>(ctas) * kSortThreads;
+    const long long i0 = static_cast<long long>(cta) * kSortThreads + threadIdx.x;
     char* base = static_cast<char*>(F.out);
     const long long head = min(static_cast<long long>((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15), F.bytes);
     const long long n16 = (F.bytes - head) / 16;
@@ -236,6 +460,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
     const long long tail = head + n16 * 16;
     if (i0 < head) base[i0] = 0;
     if (i0 < F.bytes - tail) base[tail + i0] = 0;
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
+    sort_and_fill_kernel(const SortArgs S, const FillArgs F) {
+    extern __shared__ uint4 sort_smem[];
+    const long long i0 = static_cast<long long>(blockIdx.x) * kSortThreads + threadIdx.x;
+    for (long long i = i0; i < S.ndone; i += static_cast<long long>(gridDim.x) * kSortThreads) S.done[i] = 0;
+    if (blockIdx.x < kCluster) {
+        sort_cluster(S, *reinterpret_cast<SortShared*>(sort_smem), static_cast<int>(blockIdx.x));
+        return;
+    }
+    fill_zero(F, static_cast<int>(blockIdx.x) - kCluster, static_cast<int>(gridDim.x) - kCluster);
 }
 
 // ---- gradient: sums over runs of equal tokens ------------------------------------
@@ -250,10 +486,31 @@ struct RunArgs {
     void* out;
     float* partial;        // per chunk: [0] the run that came in, [1] the run that goes on; dim fp32 each
     int nslab;             // 256-column slabs
+    unsigned* done;        // per (chunk, slab): finished pieces of the run that starts in the chunk and goes on
 };
 
 constexpr int kRunWarps = 4;
 
+// Chunks behind `chunk` (up) or before it (down) that the run of `key` reaches
+// into: up, the later chunks that start with it, down, the earlier ones that
+// end with it (whole warp; 32 chunks per look).
+__device__ __forceinline__ unsigned chunks_of_run(const RunArgs& R, unsigned chunk, unsigned key, bool up, int lane) {
+    unsigned m = 0;
+    while (true) {
+        const unsigned k = m + 1 + lane;  // so many chunks away
+        const unsigned long long at = up ? (static_cast<unsigned long long>(chunk) + k) * kChunk
+                                         : (static_cast<unsigned long long>(chunk) + 1 - k) * kChunk - 1;
+        const bool in = up ? at < R.count : k <= chunk;
+        const unsigned miss = __ballot_sync(0xffffffffu, !(in && R.keys[in ? at : 0] == key));
+        if (miss) return m + __ffs(miss) - 1;
+        m += 32;
+    }
+}
+
+// A warp adds the rows of one chunk for 256 columns.  A run inside the chunk is
+// written at once.  A run that crosses the chunk's borders leaves a partial
+// row; the warp that finishes the last of the run's chunks for these columns
+// adds the partial rows in order.
 template <typename TG, typename TO, bool VEC>
 __global__ void __launch_bounds__(kRunWarps * 32) run_sum_kernel(const RunArgs R) {
     const int lane = threadIdx.x % 32;
@@ -262,7 +519,8 @@ __global__ void __launch_bounds__(kRunWarps * 32) run_sum_kernel(const RunArgs R
     const unsigned p0 = static_cast<unsigned>(chunk) * kChunk;
     if (chunk * kChunk >= R.count) return;
     const int n = min(static_cast<unsigned>(kChunk), R.count - p0);
-    const long long c0 = (item - chunk * R.nslab) * 256;
+    const int slab = static_cast<int>(item - chunk * R.nslab);
+    const long long c0 = slab * 256ll;
     // lane i < n: pair i; lane 30: the key before the chunk; lane 31: the key after it
     unsigned k = R.vocab, q = 0;
     if (lane < n) {
@@ -279,14 +537,20 @@ __global__ void __launch_bounds__(kRunWarps * 32) run_sum_kernel(const RunArgs R
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] = 0.f;
     bool first_run = true;
+    unsigned in_key = R.vocab, out_key = R.vocab;  // runs that came in, that start here and go on
     // column of element j of this lane
     auto col = [&](int j) { return VEC ? c0 + lane * 8 + j : c0 + j * 32 + lane; };
     auto flush = [&](unsigned key, bool came_in, bool goes_on) {
         if (came_in || goes_on) {
+            (came_in ? in_key : out_key) = key;
             float* dst = R.partial + (chunk * 2 + (came_in ? 0 : 1)) * R.dim;
+            if (VEC) {
+                if (col(0) < R.dim) st8(dst + col(0), acc);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (col(j) < R.dim) dst[col(j)] = acc[j];
+                for (int j = 0; j < 8; ++j)
+                    if (col(j) < R.dim) dst[col(j)] = acc[j];
+            }
         } else {
             TO* dst = static_cast<TO*>(R.out) + static_cast<long long>(key) * R.dim;
 #pragma unroll
@@ -302,8 +566,8 @@ __global__ void __launch_bounds__(kRunWarps * 32) run_sum_kernel(const RunArgs R
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.f;
     };
-    constexpr int kBatch = 8;
-#pragma unroll
+    constexpr int kBatch = 8;  // rows whose loads are in flight at once
+#pragma unroll 1
     for (int b = 0; b < kChunk; b += kBatch) {
         if (b >= n) break;
         Raw8<TG> raw[VEC ? kBatch : 1];
@@ -325,7 +589,7 @@ __global__ void __launch_bounds__(kRunWarps * 32) run_sum_kernel(const RunArgs R
         for (int i = 0; i < kBatch; ++i) {
             const unsigned key = __shfl_sync(0xffffffffu, k, b + i);
             const unsigned after = b + i + 1 < n ? __shfl_sync(0xffffffffu, k, (b + i + 1) & 31) : next;
-            if (b + i >= n || key >= R.vocab) continue;  // the sentinels are last
+            if (b + i >= n || key >= R.vocab) continue;  // those that take no part are last
             float v[8];
             if constexpr (VEC) {
                 to_float8(raw[i], v);
@@ -336,82 +600,65 @@ __global__ void __launch_bounds__(kRunWarps * 32) run_sum_kernel(const RunArgs R
             // lanes past the last column hold nothing and store nothing
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[j] += v[j];
-            if (after != key) {
-                flush(key, first_run && prev == key, false);
+            if (after != key || b + i + 1 == n) {
+                flush(key, first_run && prev == key, after == key);
                 first_run = false;
-            } else if (b + i + 1 == n) {
-                flush(key, first_run && prev == key, true);
             }
         }
     }
-}
-
-// First index in [lo, count) whose key differs from `key` (keys are sorted).
-__device__ __forceinline__ unsigned run_end(const unsigned* keys, unsigned lo, unsigned count, unsigned key) {
-    unsigned hi = count;
-    while (lo < hi) {
-        const unsigned mid = lo + (hi - lo) / 2;
-        if (keys[mid] == key)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
-constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
-
-// One CTA per chunk: if a run starts in the chunk and goes on, add its partial
-// rows in chunk order.  Up to kJoinWarps rows are added by one thread per
-// column; a longer run is cut into kJoinWarps stretches, one per warp, whose
-// sums are added in order (the cut depends on the run alone).
-template <typename TO>
-__global__ void __launch_bounds__(kJoinThreads) run_join_kernel(const RunArgs R) {
-    __shared__ float part[kJoinWarps][32];
-    const long long chunk = blockIdx.x;
-    const unsigned p0 = static_cast<unsigned>(chunk) * kChunk;
-    const unsigned p1 = p0 + kChunk;
-    if (p1 >= R.count) return;  // the last chunk's runs end in it
-    const unsigned key = R.keys[p1 - 1];
-    if (key >= R.vocab || R.keys[p1] != key) return;
-    if (R.keys[p0] == key && p0 > 0 && R.keys[p0 - 1] == key) return;  // it started earlier
-    const unsigned end = run_end(R.keys, p1, R.count, key);
-    const long long last = (end - 1) / kChunk;  // chunk of its last pair
-    const long long m = last - chunk;           // incoming partial rows
-    const float* mine = R.partial + (chunk * 2 + 1) * R.dim;
-    const float* in = R.partial + (chunk + 1) * 2 * R.dim;  // row i at in + 2 * i * dim
-    TO* dst = static_cast<TO*>(R.out) + static_cast<long long>(key) * R.dim;
-    if (m <= kJoinWarps) {
-        for (long long c = threadIdx.x; c < R.dim; c += kJoinThreads) {
-            float s = mine[c];
-            for (long long i = 0; i < m; ++i) s += in[2 * i * R.dim + c];
-            st1(dst + c, s * R.scale);
-        }
-        return;
-    }
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const long long per = (m + kJoinWarps - 1) / kJoinWarps;
-    const long long i0 = min(per * warp, m), i1 = min(i0 + per, m);
-    for (long long c = lane; c - lane < R.dim; c += 32) {
-        float s = 0.f;
-        if (c < R.dim) {
+    if (in_key >= R.vocab && out_key >= R.vocab) return;
+    __threadfence();  // the partial rows before the counts
+    __syncwarp();
+#pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+        const unsigned key = e == 0 ? in_key : out_key;
+        if (key >= R.vocab) continue;
+        const unsigned me = static_cast<unsigned>(chunk);
+        const unsigned a = e == 0 ? me - chunks_of_run(R, me, key, false, lane) : me;
+        // a run that came in and ends here reaches no further
+        const unsigned z = e == 0 && next != key ? me : me + chunks_of_run(R, me, key, true, lane);
+        unsigned old = 0;
+        if (lane == 0) old = atomicAdd(&R.done[static_cast<long long>(a) * R.nslab + slab], 1u);
+        old = __shfl_sync(0xffffffffu, old, 0);
+        if (old != z - a) continue;  // not the last of z - a + 1 chunks
+        __threadfence();
+        const float* src = R.partial + (2ll * a + 1) * R.dim;  // the row that goes on, then every chunk's that came in
+        float s[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = 0.f;
+        TO* dst = static_cast<TO*>(R.out) + static_cast<long long>(key) * R.dim;
+        if constexpr (VEC) {
+            if (col(0) >= R.dim) continue;
+            auto add = [&](const float* p) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(p)), y = __ldcg(reinterpret_cast<const float4*>(p + 4));
+                s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
+                s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
+            };
+            add(src + col(0));
+            const float* in = src + R.dim + col(0);
 #pragma unroll 8
-            for (long long i = i0; i < i1; ++i) s += in[2 * i * R.dim + c];
+            for (unsigned i = a; i < z; ++i, in += 2 * R.dim) add(in);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] *= R.scale;
+            st8(dst + col(0), s);
+        } else {
+            for (int j = 0; j < 8; ++j)
+                if (col(j) < R.dim) s[j] = __ldcg(src + col(j));
+#pragma unroll 2
+            for (unsigned i = a; i < z; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (col(j) < R.dim) s[j] += __ldcg(src + (2ll * (i - a) + 1) * R.dim + col(j));
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (col(j) < R.dim) st1(dst + col(j), s[j] * R.scale);
         }
-        part[warp][lane] = s;
-        __syncthreads();
-        if (warp == 0 && c < R.dim) {
-            float t = mine[c];
-            for (int w = 0; w < kJoinWarps; ++w) t += part[w][lane];
-            st1(dst + c, t * R.scale);
-        }
-        __syncthreads();
     }
 }
 
 struct BwdLayout {
-    size_t keys[2], pos[2], counts, partial, total;
+    size_t keys[2], pos[2], done, partial, total;
+    size_t chunks, ndone;
 };
 
 BwdLayout bwd_layout(long long count, long long dim) {
@@ -426,18 +673,83 @@ BwdLayout bwd_layout(long long count, long long dim) {
         l.keys[i] = take(sizeof(unsigned) * count);
         l.pos[i] = take(sizeof(unsigned) * count);
     }
-    l.counts = take(sizeof(unsigned) * kCluster * kMaxBins);
-    l.partial = take(sizeof(float) * 2 * ((count + kChunk - 1) / kChunk) * dim);
+    l.chunks = (count + kChunk - 1) / kChunk;
+    l.ndone = l.chunks * ((dim + 255) / 256);
+    l.done = take(sizeof(unsigned) * l.ndone);
+    l.partial = take(sizeof(float) * 2 * l.chunks * dim);
     l.total = at;
     return l;
 }
 
+// Orders up to kClassTokens tokens into keys[0], pos[0] and fills the table with zeros.
+cudaError_t launch_class_group(const EmbedBwd& L, int classes, const BwdLayout& lay, cudaStream_t stream) {
+    char* ws = static_cast<char*>(L.workspace);
+    ClassArgs A{};
+    A.tokens = L.tokens;
+    A.tokens_i64 = L.tokens_i64;
+    A.count = static_cast<int>(L.count);
+    A.vocab = static_cast<int>(L.vocab);
+    A.classes = classes;
+    A.magic = static_cast<unsigned>(((1ull << 32) + classes - 1) / classes);
+    A.padding = L.padding;
+    A.keys = reinterpret_cast<unsigned*>(ws + lay.keys[0]);
+    A.pos = reinterpret_cast<unsigned*>(ws + lay.pos[0]);
+    A.done = reinterpret_cast<unsigned*>(ws + lay.done);
+    A.ndone = static_cast<int>(lay.ndone);
+    A.out = L.out;
+    A.dim = L.dim;
+    A.status = L.status;
+    const size_t smem = 4 * static_cast<size_t>(class_list_words(A.count));
+    auto kernel = L.out_dt == DT_F32 ? class_group_kernel<float> : class_group_kernel<__nv_bfloat16>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    kernel<<<classes, kClassThreads, smem, stream>>>(A);
+    return cudaGetLastError();
+}
+
+// The same for any number of tokens, by sorting; *side says which pair of buffers has the result.
+cudaError_t launch_sort(const EmbedBwd& L, int num_sms, const BwdLayout& lay, cudaStream_t stream, int* side) {
+    char* ws = static_cast<char*>(L.workspace);
+    SortArgs S{};
+    S.tokens = L.tokens;
+    S.tokens_i64 = L.tokens_i64;
+    S.count = static_cast<unsigned>(L.count);
+    S.vocab = static_cast<unsigned>(L.vocab);
+    S.padding = L.padding;
+    for (int i = 0; i < 2; ++i) {
+        S.keys[i] = reinterpret_cast<unsigned*>(ws + lay.keys[i]);
+        S.pos[i] = reinterpret_cast<unsigned*>(ws + lay.pos[i]);
+    }
+    int bits = 1;
+    while ((static_cast<unsigned long long>(L.vocab + 1) >> bits) != 0) ++bits;  // keys are 0 .. vocab + 1
+    S.passes = L.count > 0 ? (bits + kMaxBits - 1) / kMaxBits : 0;
+    S.digit_bits = S.passes ? (bits + S.passes - 1) / S.passes : 0;
+    S.done = reinterpret_cast<unsigned*>(ws + lay.done);
+    S.ndone = static_cast<long long>(lay.ndone);
+    S.status = L.status;
+    *side = S.passes & 1;
+    FillArgs F{L.out, L.vocab * L.dim * dtype_size(L.out_dt)};
+    // two CTAs of 1024 threads per SM; no more than the fill has 16-byte units for
+    long long fill = (F.bytes / 16 + kSortThreads - 1) / kSortThreads;
+    const long long most = static_cast<long long>(num_sms) * 2 / kCluster * kCluster - kCluster;
+    fill = fill < 1 ? 1 : (fill > most ? most : fill);
+    const unsigned grid = static_cast<unsigned>((fill + kCluster - 1) / kCluster * kCluster + kCluster);
+    const cudaError_t e = cudaFuncSetAttribute(sort_and_fill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(sizeof(SortShared)));
+    if (e != cudaSuccess) return e;
+    sort_and_fill_kernel<<<grid, kSortThreads, sizeof(SortShared), stream>>>(S, F);
+    return cudaGetLastError();
+}
+
 template <typename TG, typename TO>
-void launch_run_sum(const RunArgs& R, bool vec, unsigned blocks, cudaStream_t stream) {
+cudaError_t launch_run_sum(const RunArgs& R, bool vec, unsigned blocks, cudaStream_t stream) {
+    // launched plainly: CTAs that wait next to the zero fill slow it down
     if (vec)
         run_sum_kernel<TG, TO, true><<<blocks, kRunWarps * 32, 0, stream>>>(R);
     else
         run_sum_kernel<TG, TO, false><<<blocks, kRunWarps * 32, 0, stream>>>(R);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -467,63 +779,37 @@ size_t embedding_backward_workspace(long long count, long long dim) { return bwd
 cudaError_t launch_embedding_backward(const EmbedBwd& L, int num_sms, cudaStream_t stream, int* launches) {
     const BwdLayout lay = bwd_layout(L.count, L.dim);
     char* ws = static_cast<char*>(L.workspace);
-    SortArgs S{};
-    S.tokens = L.tokens;
-    S.tokens_i64 = L.tokens_i64;
-    S.count = static_cast<unsigned>(L.count);
-    S.vocab = static_cast<unsigned>(L.vocab);
-    S.padding = L.padding;
-    for (int i = 0; i < 2; ++i) {
-        S.keys[i] = reinterpret_cast<unsigned*>(ws + lay.keys[i]);
-        S.pos[i] = reinterpret_cast<unsigned*>(ws + lay.pos[i]);
-    }
-    S.counts = reinterpret_cast<unsigned*>(ws + lay.counts);
-    int bits = 1;
-    while ((static_cast<unsigned long long>(L.vocab) >> bits) != 0) ++bits;  // keys are 0 .. vocab
-    S.passes = L.count > 0 ? (bits + 7) / 8 : 0;
-    S.digit_bits = S.passes ? (bits + S.passes - 1) / S.passes : 0;
-    S.status = L.status;
-    FillArgs F{L.out, L.vocab * L.dim * dtype_size(L.out_dt)};
-    // two CTAs of 1024 threads per SM; no more than the fill has 16-byte units for
-    long long fill_ctas = (F.bytes / 16 + kSortThreads - 1) / kSortThreads;
-    const long long most = static_cast<long long>(num_sms) * 2 / kCluster * kCluster - kCluster;
-    fill_ctas = fill_ctas < 1 ? 1 : (fill_ctas > most ? most : fill_ctas);
-    const unsigned grid = static_cast<unsigned>((fill_ctas + kCluster - 1) / kCluster * kCluster + kCluster);
-    sort_and_fill_kernel<<<grid, kSortThreads, 0, stream>>>(S, F);
+    // the order within the call: by class and token, or by token; either keeps
+    // the tokens of a row together and their positions ascending
+    const int classes = static_cast<int>(std::min<long long>(std::min(num_sms, kMostClasses), L.vocab));
+    const bool by_class = L.count > 0 && L.count <= kClassTokens && L.vocab <= kClassVocab &&
+                          (L.vocab + classes - 1) / classes <= kClassRows;
+    int side = 0;
+    cudaError_t e = by_class ? launch_class_group(L, classes, lay, stream) : launch_sort(L, num_sms, lay, stream, &side);
     ++*launches;
-    cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || L.count == 0) return e;
 
     RunArgs R{};
-    R.keys = S.keys[S.passes & 1];
-    R.pos = S.pos[S.passes & 1];
-    R.count = S.count;
-    R.vocab = S.vocab;
+    R.keys = reinterpret_cast<const unsigned*>(ws + lay.keys[side]);
+    R.pos = reinterpret_cast<const unsigned*>(ws + lay.pos[side]);
+    R.count = static_cast<unsigned>(L.count);
+    R.vocab = static_cast<unsigned>(L.vocab);
     R.grad = L.grad;
     R.ld = L.ld;
     R.dim = L.dim;
     R.scale = L.scale;
     R.out = L.out;
     R.partial = reinterpret_cast<float*>(ws + lay.partial);
+    R.done = reinterpret_cast<unsigned*>(ws + lay.done);
     R.nslab = static_cast<int>((L.dim + 255) / 256);
-    const long long nchunks = (L.count + kChunk - 1) / kChunk;
-    const unsigned blocks = static_cast<unsigned>((nchunks * R.nslab + kRunWarps - 1) / kRunWarps);
+    const unsigned blocks = static_cast<unsigned>((lay.ndone + kRunWarps - 1) / kRunWarps);
     const bool vec = rows_vec_ok(L.grad, L.ld, L.grad_dt) && rows_vec_ok(L.out, L.dim, L.out_dt) && L.dim % 8 == 0;
+    ++*launches;
     if (L.grad_dt == DT_F32)
-        L.out_dt == DT_F32 ? launch_run_sum<float, float>(R, vec, blocks, stream)
-                           : launch_run_sum<float, __nv_bfloat16>(R, vec, blocks, stream);
-    else
-        L.out_dt == DT_F32 ? launch_run_sum<__nv_bfloat16, float>(R, vec, blocks, stream)
-                           : launch_run_sum<__nv_bfloat16, __nv_bfloat16>(R, vec, blocks, stream);
-    ++*launches;
-    e = cudaGetLastError();
-    if (e != cudaSuccess || nchunks < 2) return e;
-    if (L.out_dt == DT_F32)
-        run_join_kernel<float><<<static_cast<unsigned>(nchunks), kJoinThreads, 0, stream>>>(R);
-    else
-        run_join_kernel<__nv_bfloat16><<<static_cast<unsigned>(nchunks), kJoinThreads, 0, stream>>>(R);
-    ++*launches;
-    return cudaGetLastError();
+        return L.out_dt == DT_F32 ? launch_run_sum<float, float>(R, vec, blocks, stream)
+                                  : launch_run_sum<float, __nv_bfloat16>(R, vec, blocks, stream);
+    return L.out_dt == DT_F32 ? launch_run_sum<__nv_bfloat16, float>(R, vec, blocks, stream)
+                              : launch_run_sum<__nv_bfloat16, __nv_bfloat16>(R, vec, blocks, stream);
 }
 
 }  // namespace muon
