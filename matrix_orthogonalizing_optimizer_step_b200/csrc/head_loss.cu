@@ -15,9 +15,16 @@
 // the bound, on the tensor cores, except for short batches, where reading the
 // weight is.
 //
-// Tokens whose target is ignored take no part: the rows that count are first
-// copied together, so they cost nothing in the products, and whatever an
-// ignored row holds (infinities, NaN) reaches no result.
+// Tokens whose target is ignored take no part: if there are any, the rows that
+// count are first copied together, so they cost nothing in the products, and
+// whatever an ignored row holds (infinities, NaN) reaches no result.
+//
+// P is rounded to bf16 for the two products that read it.  Its common factor,
+// the largest |dloss|, is left out and multiplied into the fp32 sums instead:
+// with equal dloss (the mean's gradient) a target's entry is then p - 1, not
+// dloss (p - 1), whose rounding would be off the same way in every row.  What
+// the rounding takes off the target's entry, the largest of its row, is added
+// back to dh in fp32.
 //
 // The products use CTA pairs (tcgen05 cta_group::2, M = 256, N = 256, K = 16,
 // bf16 operands, fp32 accumulation in tensor memory) fed by TMA:
@@ -37,6 +44,7 @@
 
 #include "epilogue.cuh"
 #include "lane.h"
+#include "pdl.h"
 #include "ptx.cuh"
 
 namespace muon {
@@ -83,13 +91,17 @@ struct HeadGemm {
     CUtensorMap b;      // STATS, PROB: weight, K-major.               GRAD: weight, MN-major (dh)
     CUtensorMap a2;     // GRAD: P, MN-major (dW)
     CUtensorMap b2;     // GRAD: copied hidden rows, MN-major (dW)
+    CUtensorMap all;    // the caller's hidden rows as a or b2: read instead where every row counts
     CUtensorMap o;      // PROB: P store.                              GRAD: fp32 dh slots
     CUtensorMap o2;     // GRAD: dW store
     const int* nvalid;  // rows that count
     unsigned* ticket;   // next unclaimed tile
     const int* target;  // per copied row
     const float* lse;
-    const float* dloss;
+    const float* dloss; // per copied row, over *scale
+    const float* scale; // GRAD: the common factor of dloss
+    float* rest;        // PROB: per copied row, what rounding took off the target's entry
+    int tokens;         // all rows
     float2* part;       // STATS: (max, sum) [2 * vocab tiles][row_pitch]
     float* tlogit;      // STATS: the target's logit per copied row
     long long row_pitch;
@@ -226,6 +238,7 @@ __device__ void producer(const HeadGemm& L, int nvalid, uint8_t* tiles_smem, Sha
     volatile int* abort_flag = &sh->abort;
     const unsigned long long lim = L.wait_ns;
     const bool leader = rank == 0;
+    const CUtensorMap* hidden = nvalid == L.tokens ? &L.all : (MODE == GRAD ? &L.b2 : &L.a);
     int stage = 0;
     uint32_t phase = 0, issued = 0;
     bool ok = true;
@@ -250,7 +263,7 @@ __device__ void producer(const HeadGemm& L, int nvalid, uint8_t* tiles_smem, Sha
             if (leader) mbar_arrive_expect_tx(&sh->full[stage], 2 * STAGE_BYTES);
             const int k = (x.k0 + i) * BK;
             if (MODE != GRAD) {
-                tma_load_3d_pair(sa, &L.a, full, k, arow, 0);
+                tma_load_3d_pair(sa, hidden, full, k, arow, 0);
                 tma_load_3d_pair(sb, &L.b, full, k, L.v0 + brow, 0);
             } else if (!x.dw) {
                 tma_load_3d_pair(sa, &L.a, full, k, arow, 0);
@@ -263,7 +276,7 @@ __device__ void producer(const HeadGemm& L, int nvalid, uint8_t* tiles_smem, Sha
                     tma_load_3d_pair(sa + j * MN_BLOCK_BYTES, &L.a2, full, arow + 64 * j, k, 0);
 #pragma unroll
                 for (int j = 0; j < BNH / 64; ++j)
-                    tma_load_3d_pair(sb + j * MN_BLOCK_BYTES, &L.b2, full, brow + 64 * j, k, 0);
+                    tma_load_3d_pair(sb + j * MN_BLOCK_BYTES, hidden, full, brow + 64 * j, k, 0);
             }
             ++issued;
             if (++stage == STAGES) {
@@ -424,6 +437,7 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
             break;
         }
         tc_fence_after();
+        const float scale = MODE == GRAD ? *L.scale : 1.f;
         float m = -INFINITY, s = 0.f;  // STATS: maximum and sum of exp(l - m)
 #pragma unroll 1
         for (int c = 0; c < PART_COLS; c += 32) {
@@ -463,12 +477,20 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
             } else if (MODE == PROB) {
                 const int at = y - col0;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    float p = exp_diff(v[j] - lse);
-                    if (j == at) p -= 1.f;
-                    // rows behind the last that counts and columns behind the
-                    // vocabulary hold zeros (whatever the accumulator holds)
-                    v[j] = row < nvalid && j < ncols ? dl * p : 0.f;
+                for (int j = 0; j < 32; ++j) v[j] = dl * exp_diff(v[j] - lse);
+                if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+                    float g = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j == at) g = v[j] -= dl;
+                    if (at >= 0 && at < 32) L.rest[row] = g - __bfloat162float(__float2bfloat16_rn(g));
+                }
+                // rows behind the last that counts and columns behind the
+                // vocabulary hold zeros, whatever the accumulator holds
+                if (row0 + 32 > nvalid || ncols < 32) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (row >= nvalid || j >= ncols) v[j] = 0.f;
                 }
                 uint4 u[4];
 #pragma unroll
@@ -476,6 +498,8 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
                 store_box(&L.o, u, col0, row0, 0, false);
             } else if (x.dw) {
                 if (L.v0 + row0 >= L.vocab) continue;  // warp-uniform
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= scale;
                 uint4 u[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) u[i] = pack8(v + 8 * i, DT_BF16);
@@ -515,6 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     Shared* sh = reinterpret_cast<Shared*>(store_smem + STORE_BYTES);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_cta_rank();
+    allow_successor();
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&sh->full[s], 1);
@@ -542,7 +567,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = sh->tmem_base;
-    const int nvalid = *L.nvalid;
+    wait_predecessor();
+    const int nvalid = *reinterpret_cast<const volatile int*>(L.nvalid);
     if (warp == 0) {
         if (lane == 0) producer<MODE>(L, nvalid, tiles_smem, sh, rank);
     } else if (warp == 1) {
@@ -578,14 +604,15 @@ struct RowsArgs {
     int* index;             // per token: its copied row, kIgnored or kBadTarget
     int* target;            // per copied row
     float* lse;             // per copied row (backward)
-    float* dloss;
+    float* dloss;           // over *scale
+    float* scale;           // or null
     int* nvalid;
     unsigned* tickets;
     int ntickets;
     DeviceStatus* status;
 };
 
-constexpr int kRowsPerCta = 32;
+constexpr int kRowsPerCta = 8;
 constexpr int kRowsThreads = 256;
 
 __device__ __forceinline__ long long target_at(const RowsArgs& A, int t) {
@@ -595,48 +622,60 @@ __device__ __forceinline__ bool counts(const RowsArgs& A, long long y) {
     return y != A.ignore && y >= 0 && y < A.vocab;
 }
 
-// Copies the rows that count together, in order; the copied rows up to the
-// next multiple of 256 are zeroed.  A CTA finds the place of its rows by
-// counting all targets before them.
+// Finds the place of every row that counts among those that do and, if some do
+// not, copies the ones that do together, in order; the copied rows up to the
+// next multiple of 256 are zeroed.  A CTA of kRowsPerCta tokens counts all
+// targets before them itself.
 __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs A) {
-    __shared__ int red[2][kRowsThreads / 32];
+    constexpr int kWarps = kRowsThreads / 32;
+    __shared__ int red[2][kWarps];
+    __shared__ float red_dl[kWarps];
     __shared__ int dst_of[kRowsPerCta];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    allow_successor();
     const int t0 = blockIdx.x * kRowsPerCta;
     int before = 0, all = 0;
+    float top = 0.f;
+#pragma unroll 8
     for (int t = tid; t < A.tokens; t += kRowsThreads) {
-        const int c = counts(A, target_at(A, t)) ? 1 : 0;
-        all += c;
-        if (t < t0) before += c;
+        const bool c = counts(A, target_at(A, t));
+        all += c ? 1 : 0;
+        if (t < t0) before += c ? 1 : 0;
+        if (A.dloss_in && c) top = fmaxf(top, fabsf(A.dloss_in[t]));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         before += __shfl_xor_sync(0xffffffffu, before, o);
         all += __shfl_xor_sync(0xffffffffu, all, o);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
     if (lane == 0) {
         red[0][warp] = before;
         red[1][warp] = all;
+        red_dl[warp] = top;
     }
     __syncthreads();
     before = all = 0;
-    for (int w = 0; w < kRowsThreads / 32; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         before += red[0][w];
         all += red[1][w];
+        top = fmaxf(top, red_dl[w]);
     }
+    // the common factor of dloss; 1 where it would not be one
+    const float scale = top > 0.f && top <= 3.4e38f ? top : 1.f;
     if (warp == 0) {
         const int t = t0 + lane;
-        const bool in = t < A.tokens;
+        const bool in = lane < kRowsPerCta && t < A.tokens;
         const long long y = in ? target_at(A, t) : A.ignore;
         const bool on = in && counts(A, y);
         const unsigned mask = __ballot_sync(0xffffffffu, on);
         const int r = before + __popc(mask & ((1u << lane) - 1));
-        dst_of[lane] = on ? r : -1;
+        if (lane < kRowsPerCta) dst_of[lane] = on ? r : -1;
         if (on) {
             A.target[r] = static_cast<int>(y);
             if (A.dloss_in) {
                 A.lse[r] = A.lse_in[t];
-                A.dloss[r] = A.dloss_in[t];
+                A.dloss[r] = A.dloss_in[t] / scale;
             }
         }
         if (in) {
@@ -649,22 +688,25 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs 
         }
     }
     if (blockIdx.x == 0) {
-        if (tid == 0) *A.nvalid = all;
+        if (tid == 0) {
+            *A.nvalid = all;
+            if (A.scale) *A.scale = scale;
+        }
         for (int i = tid; i < A.ntickets; i += kRowsThreads) A.tickets[i] = 0;
     }
+    if (all == A.tokens) return;  // the products read the caller's rows
     __syncthreads();
     const int units = A.dim / 8;  // 16-byte units of a row
-    for (int i = warp; i < kRowsPerCta; i += kRowsThreads / 32) {
-        const int r = dst_of[i];
-        if (r < 0) continue;
-        const uint4* src = reinterpret_cast<const uint4*>(A.hidden + (t0 + i) * A.ldh);
-        uint4* dst = reinterpret_cast<uint4*>(A.rows + static_cast<long long>(r) * A.dim);
-#pragma unroll 4
+    static_assert(kRowsPerCta == kWarps, "a warp copies a row");
+    if (dst_of[warp] >= 0) {
+        const uint4* src = reinterpret_cast<const uint4*>(A.hidden + (t0 + warp) * A.ldh);
+        uint4* dst = reinterpret_cast<uint4*>(A.rows + static_cast<long long>(dst_of[warp]) * A.dim);
+#pragma unroll 8
         for (int u = lane; u < units; u += 32) dst[u] = src[u];
     }
     // rows behind the last
     const int end = max(BMP, (all + BMP - 1) / BMP * BMP);
-    for (int r = all + blockIdx.x * (kRowsThreads / 32) + warp; r < end; r += gridDim.x * (kRowsThreads / 32)) {
+    for (int r = all + blockIdx.x * kWarps + warp; r < end; r += gridDim.x * kWarps) {
         uint4* dst = reinterpret_cast<uint4*>(A.rows + static_cast<long long>(r) * A.dim);
         for (int u = lane; u < units; u += 32) dst[u] = make_uint4(0, 0, 0, 0);
     }
@@ -682,6 +724,7 @@ __global__ void __launch_bounds__(32 * kJoinGroups)
     __shared__ float2 red[kJoinGroups][33];
     const int lane = threadIdx.x % 32, g = threadIdx.x / 32;
     const int t = blockIdx.x * 32 + lane;
+    wait_predecessor();
     const int r = t < tokens ? index[t] : kIgnored;
     float m = -INFINITY, s = 0.f;
     auto join = [&](float2 p) {
@@ -704,13 +747,18 @@ __global__ void __launch_bounds__(32 * kJoinGroups)
     loss[t] = r >= 0 ? l - tlogit[r] : (r == kBadTarget ? nan : 0.f);
 }
 
-// dh: the sum of a row's slots, rounded to bf16; zero for tokens that take no part.
+// dh: the sum of a row's slots and what rounding took off the target's entry,
+// times the common factor, rounded to bf16; zero for tokens that take no part.
 __global__ void __launch_bounds__(128)
-    head_dhidden_kernel(const float* slots, int nslots, long long slot_pitch, const int* index, int dim,
+    head_dhidden_kernel(const float* slots, int nslots, long long slot_pitch, const int* index, const int* target,
+                        const float* rest, const float* scale, const __nv_bfloat16* weight, int dim,
                         __nv_bfloat16* dhidden) {
     const int t = blockIdx.x;
+    wait_predecessor();
     const int r = index[t];
     __nv_bfloat16* dst = dhidden + static_cast<long long>(t) * dim;
+    const float f = *scale, d = r >= 0 ? rest[r] : 0.f;
+    const __nv_bfloat16* w = weight + static_cast<long long>(r >= 0 ? target[r] : 0) * dim;
     for (int c = threadIdx.x * 8; c < dim; c += 128 * 8) {
         float v[8];
 #pragma unroll
@@ -722,6 +770,10 @@ __global__ void __launch_bounds__(128)
                 v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
                 v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
             }
+            float x[8];
+            unpack8(*reinterpret_cast<const uint4*>(w + c), DT_BF16, x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = f * fmaf(d, x[j], v[j]);
         }
         *reinterpret_cast<uint4*>(dst + c) = pack8(v, DT_BF16);
     }
@@ -797,8 +849,7 @@ cudaError_t launch_gemm(const HeadGemm& G, long long tiles, cudaStream_t stream)
     const int pairs = max_pairs<MODE>();
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     const unsigned grid = 2 * static_cast<unsigned>(std::min<long long>(pairs, tiles));
-    head_gemm_kernel<MODE><<<grid, NUM_THREADS, SMEM_BYTES, stream>>>(G);
-    return cudaGetLastError();
+    return launch_dependent(head_gemm_kernel<MODE>, dim3(grid), NUM_THREADS, SMEM_BYTES, stream, G);
 }
 
 constexpr int kPairsNominal = 74;             // CTA pairs of a B200, for the split of short batches
@@ -810,7 +861,7 @@ struct Layout {
     long long vtiles;     // 256-wide tiles of the vocabulary
     long long piece_tiles, pieces;
     int splits, split_slices;  // of the first piece
-    size_t rows, index, target, nvalid, tickets, part, tlogit, lse, dloss, p, slots, total;
+    size_t rows, index, target, nvalid, tickets, part, tlogit, lse, dloss, rest, scale, p, slots, total;
     int ntickets;
 };
 
@@ -850,6 +901,8 @@ Layout layout(long long tokens, long long vocab, long long dim, bool backward) {
         l.ntickets = static_cast<int>(2 * l.pieces);
         l.lse = take(4ull * l.tpad);
         l.dloss = take(4ull * l.tpad);
+        l.rest = take(4ull * l.tpad);
+        l.scale = take(4);
         l.p = take(2ull * l.tpad * l.piece_tiles * BN);
         l.slots = take(4ull * l.splits * l.tpad * dim);
     }
@@ -877,6 +930,7 @@ cudaError_t launch_rows(const HeadLoss& L, const Layout& l, bool backward, cudaS
         A.dloss_in = L.dloss;
         A.lse = reinterpret_cast<float*>(ws + l.lse);
         A.dloss = reinterpret_cast<float*>(ws + l.dloss);
+        A.scale = reinterpret_cast<float*>(ws + l.scale);
     }
     A.nvalid = reinterpret_cast<int*>(ws + l.nvalid);
     A.tickets = reinterpret_cast<unsigned*>(ws + l.tickets);
@@ -893,6 +947,7 @@ HeadGemm gemm_args(const HeadLoss& L, const Layout& l) {
     G.target = reinterpret_cast<const int*>(ws + l.target);
     G.vocab = static_cast<int>(L.vocab);
     G.dim = static_cast<int>(L.dim);
+    G.tokens = static_cast<int>(L.tokens);
     G.vtiles = static_cast<int>(l.vtiles);
     G.row_pitch = l.tpad;
     G.status = L.status;
@@ -915,6 +970,7 @@ cudaError_t launch_head_loss(const HeadLoss& L, cudaStream_t stream, int* launch
     char* ws = static_cast<char*>(L.workspace);
     HeadGemm G = gemm_args(L, l);
     if (!encode(&G.a, BOX_K, ws + l.rows, false, L.dim, l.tpad, L.dim) ||
+        !encode(&G.all, BOX_K, L.hidden, false, L.dim, L.tokens, L.ldh) ||
         !encode(&G.b, BOX_K, L.weight, false, L.dim, L.vocab, L.dim)) {
         *why = "tensor map encoding failed";
         return cudaErrorInvalidValue;
@@ -927,11 +983,10 @@ cudaError_t launch_head_loss(const HeadLoss& L, cudaStream_t stream, int* launch
     e = launch_gemm<STATS>(G, l.tpad / BMP * l.vtiles, stream);
     if (e != cudaSuccess) return e;
     const int nparts = static_cast<int>((L.vocab + PART_COLS - 1) / PART_COLS);
-    head_join_kernel<<<static_cast<unsigned>((L.tokens + 31) / 32), 32 * kJoinGroups, 0, stream>>>(
-        G.part, nparts, l.tpad, G.tlogit, reinterpret_cast<const int*>(ws + l.index), static_cast<int>(L.tokens), L.loss,
-        L.lse);
     *launches += 3;
-    return cudaGetLastError();
+    return launch_dependent(head_join_kernel, dim3(static_cast<unsigned>((L.tokens + 31) / 32)), 32 * kJoinGroups, 0,
+                            stream, G.part, nparts, l.tpad, G.tlogit, reinterpret_cast<const int*>(ws + l.index),
+                            static_cast<int>(L.tokens), L.loss, L.lse);
 }
 
 cudaError_t launch_head_loss_backward(const HeadLoss& L, cudaStream_t stream, int* launches, const char** why) {
@@ -945,7 +1000,11 @@ cudaError_t launch_head_loss_backward(const HeadLoss& L, cudaStream_t stream, in
     HeadGemm P = gemm_args(L, l), D = P;
     P.lse = reinterpret_cast<const float*>(ws + l.lse);
     P.dloss = reinterpret_cast<const float*>(ws + l.dloss);
+    P.rest = reinterpret_cast<float*>(ws + l.rest);
+    D.scale = reinterpret_cast<const float*>(ws + l.scale);
     const bool ok = encode(&P.a, BOX_K, ws + l.rows, false, L.dim, l.tpad, L.dim) &&
+                    encode(&P.all, BOX_K, L.hidden, false, L.dim, L.tokens, L.ldh) &&
+                    encode(&D.all, BOX_MN, L.hidden, false, L.dim, L.tokens, L.ldh) &&
                     encode(&P.b, BOX_K, L.weight, false, L.dim, L.vocab, L.dim) &&
                     encode(&P.o, BOX_STORE, ws + l.p, false, pitch, l.tpad, pitch) &&
                     encode(&D.a, BOX_K, ws + l.p, false, pitch, l.tpad, pitch) &&
@@ -981,12 +1040,12 @@ cudaError_t launch_head_loss_backward(const HeadLoss& L, cudaStream_t stream, in
         *launches += 2;
     }
     if (!L.dhidden) return cudaSuccess;
-    head_dhidden_kernel<<<static_cast<unsigned>(L.tokens), 128, 0, stream>>>(
-        reinterpret_cast<const float*>(ws + l.slots), l.splits, l.tpad * L.dim,
-        reinterpret_cast<const int*>(ws + l.index), static_cast<int>(L.dim),
-        static_cast<__nv_bfloat16*>(L.dhidden));
     ++*launches;
-    return cudaGetLastError();
+    return launch_dependent(head_dhidden_kernel, dim3(static_cast<unsigned>(L.tokens)), 128, 0, stream,
+                            reinterpret_cast<const float*>(ws + l.slots), l.splits, l.tpad * L.dim,
+                            reinterpret_cast<const int*>(ws + l.index), reinterpret_cast<const int*>(ws + l.target),
+                            P.rest, D.scale, static_cast<const __nv_bfloat16*>(L.weight), static_cast<int>(L.dim),
+                            static_cast<__nv_bfloat16*>(L.dhidden));
 }
 
 }  // namespace muon
