@@ -337,7 +337,17 @@ def muon_version():
     return int(lib().muon_version())
 
 
-from ._lane import (  # noqa: E402,F401
-    muon_embedding, muon_embedding_backward, muon_head_loss, muon_head_loss_backward, muon_layer_norm,
-    muon_layer_norm_backward,
-)
+# The AdamW lane's layers, bound by a compiled module that is loaded when one
+# of them is first used (it does not exist before the first build).
+_LANE = ("muon_embedding", "muon_embedding_backward", "muon_layer_norm", "muon_layer_norm_backward", "muon_head_loss",
+         "muon_head_loss_backward")
+
+
+def __getattr__(name):
+    if name in _LANE:
+        lib()  # says how to build what is missing
+        from . import _lane_native
+        for n in _LANE:
+            globals()[n] = getattr(_lane_native, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -4,6 +4,9 @@ Every .cu / .cpp file under csrc/ is compiled to an object under _build/ and
 the objects are linked into libmuon.so next to this file (the CUDA runtime is
 linked statically, so the library loads on a machine without a GPU driver;
 the driver is reached at run time through cudaGetDriverEntryPoint).
+
+csrc/binding/ holds the Python module of the AdamW lane's layers, compiled
+against torch's headers and linked to libmuon.so by its place next to it.
 """
 from __future__ import annotations
 
@@ -19,6 +22,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmuon.so")
+BINDING = os.path.join(CSRC, "binding", "lane_torch.cpp")
+EXT = os.path.join(HERE, "_lane_native.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CFLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -48,6 +53,30 @@ def _stale(target, deps):
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_command():
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ["g++", "-std=c++17", "-O2", "-shared", "-fPIC", "-fvisibility=hidden", "-DTORCH_EXTENSION_NAME=_lane_native",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *["-isystem" + i for i in inc],
+            BINDING, "-o", EXT, "-L" + HERE, "-l:libmuon.so", "-Wl,-rpath,$ORIGIN", "-L" + lib,
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python"]
+
+
+def build_binding(verbose=False, force=False):
+    if force or _stale(EXT, [BINDING, os.path.join(ROOT, "include", "muon.h")]):
+        res = subprocess.run(_binding_command(), capture_output=True, text=True)
+        if verbose or res.returncode != 0:
+            sys.stderr.write(" ".join(_binding_command()) + "\n" + res.stdout + res.stderr)
+        if res.returncode != 0:
+            raise RuntimeError("build of the binding failed")
+    return EXT
+
+
 def build(verbose=False, force=False, extra_flags=()):
     nvcc = _nvcc()
     os.makedirs(BUILD, exist_ok=True)
@@ -72,6 +101,7 @@ def build(verbose=False, force=False, extra_flags=()):
         if res.returncode != 0:
             sys.stderr.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
             raise RuntimeError("link of libmuon.so failed")
+    build_binding(verbose, force)
     return LIB
 
 
