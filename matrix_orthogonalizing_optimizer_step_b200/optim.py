@@ -15,6 +15,12 @@ elementwise launch as the Muon momentum pass, followed by the Newton-Schulz
 launches.  Otherwise each group takes its own call (muon_step,
 muon_adamw_step).  Gradients may be fp32 or bf16; the installed config's
 gradient and parameter dtypes are set to match.
+
+An AdamW parameter's gradient may be row-sparse, as torch.nn.Embedding(...,
+sparse=True) leaves it: (token, row) pairs, tokens repeated.  The step sums it
+into a dense gradient with muon_embedding_backward (in a buffer kept per
+parameter) and goes on as with a dense one: moments and weight decay reach
+every row.
 """
 from __future__ import annotations
 
@@ -59,6 +65,7 @@ class MuonHybrid(torch.optim.Optimizer):
             groups.append(dict(params=ap, kind="adamw", lr=adamw_lr, betas=adamw_betas, eps=adamw_eps,
                                weight_decay=adamw_weight_decay))
         super().__init__(groups, {})
+        self._row_grads = {}  # dense gradients of parameters whose gradient is row-sparse
 
     @torch.no_grad()
     def step(self, closure=None):
@@ -74,6 +81,8 @@ class MuonHybrid(torch.optim.Optimizer):
                 raise TypeError("one gradient dtype and one parameter dtype per group, each fp32 or bf16")
             dts = (gdt.pop(), pdt.pop())
             if g["kind"] == "muon":
+                if any(p.grad.is_sparse for p in ps):
+                    raise TypeError("Muon parameters need dense gradients")
                 lanes["muon"] = (g, dts, self._muon_lane(ps))
             else:
                 lanes["adamw"] = (g, dts, self._adamw_lane(ps))
@@ -126,7 +135,23 @@ class MuonHybrid(torch.optim.Optimizer):
             st["step"] += 1
             lists = by_step.setdefault(st["step"], ([], [], [], []))
             lists[0].append(p.view(-1))
-            lists[1].append(p.grad.view(-1))
+            lists[1].append(self._dense_grad(p).view(-1))
             lists[2].append(st["exp_avg"])
             lists[3].append(st["exp_avg_sq"])
         return by_step
+
+    def _dense_grad(self, p):
+        g = p.grad
+        if not g.is_sparse:
+            return g
+        if p.dim() != 2 or g.sparse_dim() != 1:
+            raise TypeError("a sparse gradient must hold rows of a 2-D parameter")
+        from . import muon_embedding_backward
+        # not coalesced: the kernel sums equal tokens itself
+        tokens, rows = g._indices()[0].contiguous(), g._values().contiguous()
+        kept = self.__dict__.setdefault("_row_grads", {})
+        out = kept.get(p)
+        if out is not None and (out.dtype != rows.dtype or out.shape != p.shape):
+            out = None
+        kept[p] = muon_embedding_backward(tokens, rows, p.shape[0], out=out)
+        return kept[p]
