@@ -475,7 +475,7 @@ MUON_API int muon_head_loss(const void* hidden, long long ld_hidden, const void*
  * computed).  lse is the forward call's; dloss (fp32, one per
  * token) is the gradient of the per-token loss.  p is rounded to bf16 for the
  * two products (as the tensor cores take it), whose sums are fp32.  The
- * vocabulary is walked in pieces whose p fits in 256 MiB (one 256-column tile
+ * vocabulary is walked in pieces whose p fits in 512 MiB (one 256-column tile
  * at least).  dhidden is 0 for ignored tokens, and so is their share of
  * dweight whatever their dloss and hidden rows hold.
  */

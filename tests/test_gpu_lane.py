@@ -374,7 +374,7 @@ def test_head_loss_bad_targets_are_reported():
 def test_head_loss_pieces():
     """A batch whose probabilities exceed the piece size: several pieces of the
     vocabulary, the last one shorter, against the 64-bit form."""
-    check_head(*head_case(4100, 33000, 64, 90, ignored=0.1))
+    check_head(*head_case(8200, 33000, 64, 90, ignored=0.1))
     status_ok()
 
 
