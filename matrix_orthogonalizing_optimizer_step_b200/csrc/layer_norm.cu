@@ -60,9 +60,11 @@ struct RowShape {
     static constexpr bool keep = NE <= 24 && !(ARRAYS == 2 && W == 16);
     static constexpr int threads = RowCta<W>::threads;
     static constexpr int stage_bytes = ARRAYS * NU * threads * 16;
-    // rows in flight per row group: up to 4, in about 48 KB per CTA
-    static constexpr int fit = 49152 / stage_bytes;
-    static constexpr int stages = ACCESS == DIRECT ? 0 : (fit > 4 ? 4 : (fit < 2 ? 2 : fit));
+    // rows in flight per row group, in about 48 KB per CTA: up to 3 forward
+    // (16384 x 4096 bf16: 47.5 us; 2: 49.9, 4: 49.0), 2 backward, where the
+    // registers hold more (16384 x 768: 19.0 us; 3 and 4: 20.5)
+    static constexpr int fit = 49152 / stage_bytes, most = ARRAYS == 1 ? 3 : 2;
+    static constexpr int stages = ACCESS == DIRECT ? 0 : (fit > most ? most : (fit < 2 ? 2 : fit));
     // the ring, or the sums of a backward CTA's row groups
     static constexpr int comb_bytes = ARRAYS == 2 && RowCta<W>::rows > 1 ? RowCta<W>::rows * 2 * W * 32 * NE * 4 : 0;
     static constexpr int ring_bytes = stages * stage_bytes;
@@ -625,7 +627,9 @@ int backward_parts_bound(long long rows, int num_sms) {
 template <typename K>
 cudaError_t persistent_grid(K kernel, int threads, int smem, int num_sms, int& per_sm, long long need, int most_per_sm,
                             unsigned& grid) {
-    if (smem > 0) {
+    // above the 48 KB that every kernel may use (static shared memory counts
+    // too) the limit is raised, for the current device, on every call
+    if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
