@@ -612,8 +612,9 @@ struct RowsArgs {
     DeviceStatus* status;
 };
 
-constexpr int kRowsPerCta = 8;
 constexpr int kRowsThreads = 256;
+constexpr int kRowsWarps = kRowsThreads / 32;
+constexpr int kRowsMostCtas = 1024;  // each reads all targets: 8 bytes x tokens x 1024 from L2 at most
 
 __device__ __forceinline__ long long target_at(const RowsArgs& A, int t) {
     return A.targets_i64 ? static_cast<const long long*>(A.targets)[t] : static_cast<const int*>(A.targets)[t];
@@ -624,16 +625,16 @@ __device__ __forceinline__ bool counts(const RowsArgs& A, long long y) {
 
 // Finds the place of every row that counts among those that do and, if some do
 // not, copies the ones that do together, in order; the copied rows up to the
-// next multiple of 256 are zeroed.  A CTA of kRowsPerCta tokens counts all
-// targets before them itself.
-__global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs A) {
-    constexpr int kWarps = kRowsThreads / 32;
+// next multiple of 256 are zeroed.  A CTA has `per` tokens (a multiple of 8)
+// and counts all targets before them itself.
+__global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs A, int per) {
+    constexpr int kWarps = kRowsWarps;
     __shared__ int red[2][kWarps];
     __shared__ float red_dl[kWarps];
-    __shared__ int dst_of[kRowsPerCta];
+    __shared__ int dst_of[32];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     allow_successor();
-    const int t0 = blockIdx.x * kRowsPerCta;
+    const int t0 = blockIdx.x * per, t1 = min(t0 + per, A.tokens);
     int before = 0, all = 0;
     float top = 0.f;
 #pragma unroll 8
@@ -663,30 +664,6 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs 
     }
     // the common factor of dloss; 1 where it would not be one
     const float scale = top > 0.f && top <= 3.4e38f ? top : 1.f;
-    if (warp == 0) {
-        const int t = t0 + lane;
-        const bool in = lane < kRowsPerCta && t < A.tokens;
-        const long long y = in ? target_at(A, t) : A.ignore;
-        const bool on = in && counts(A, y);
-        const unsigned mask = __ballot_sync(0xffffffffu, on);
-        const int r = before + __popc(mask & ((1u << lane) - 1));
-        if (lane < kRowsPerCta) dst_of[lane] = on ? r : -1;
-        if (on) {
-            A.target[r] = static_cast<int>(y);
-            if (A.dloss_in) {
-                A.lse[r] = A.lse_in[t];
-                A.dloss[r] = A.dloss_in[t] / scale;
-            }
-        }
-        if (in) {
-            const bool bad = !on && y != A.ignore;
-            A.index[t] = on ? r : (bad ? kBadTarget : kIgnored);
-            if (bad) {
-                atomicMin(&A.status->first_bad_token, t);
-                atomicOr(&A.status->bits, ST_INDEX);
-            }
-        }
-    }
     if (blockIdx.x == 0) {
         if (tid == 0) {
             *A.nvalid = all;
@@ -694,16 +671,45 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs 
         }
         for (int i = tid; i < A.ntickets; i += kRowsThreads) A.tickets[i] = 0;
     }
-    if (all == A.tokens) return;  // the products read the caller's rows
-    __syncthreads();
     const int units = A.dim / 8;  // 16-byte units of a row
-    static_assert(kRowsPerCta == kWarps, "a warp copies a row");
-    if (dst_of[warp] >= 0) {
-        const uint4* src = reinterpret_cast<const uint4*>(A.hidden + (t0 + warp) * A.ldh);
-        uint4* dst = reinterpret_cast<uint4*>(A.rows + static_cast<long long>(dst_of[warp]) * A.dim);
+    for (int s0 = t0; s0 < t1; s0 += 32) {
+        if (warp == 0) {
+            const int t = s0 + lane;
+            const bool in = t < t1;
+            const long long y = in ? target_at(A, t) : A.ignore;
+            const bool on = in && counts(A, y);
+            const unsigned mask = __ballot_sync(0xffffffffu, on);
+            const int r = before + __popc(mask & ((1u << lane) - 1));
+            dst_of[lane] = on ? r : -1;
+            before += __popc(mask);
+            if (on) {
+                A.target[r] = static_cast<int>(y);
+                if (A.dloss_in) {
+                    A.lse[r] = A.lse_in[t];
+                    A.dloss[r] = A.dloss_in[t] / scale;
+                }
+            }
+            if (in) {
+                const bool bad = !on && y != A.ignore;
+                A.index[t] = on ? r : (bad ? kBadTarget : kIgnored);
+                if (bad) {
+                    atomicMin(&A.status->first_bad_token, t);
+                    atomicOr(&A.status->bits, ST_INDEX);
+                }
+            }
+        }
+        if (all == A.tokens) continue;  // the products read the caller's rows
+        __syncthreads();
+        for (int i = warp; i < min(32, t1 - s0); i += kWarps) {
+            if (dst_of[i] < 0) continue;
+            const uint4* src = reinterpret_cast<const uint4*>(A.hidden + (s0 + i) * A.ldh);
+            uint4* dst = reinterpret_cast<uint4*>(A.rows + static_cast<long long>(dst_of[i]) * A.dim);
 #pragma unroll 8
-        for (int u = lane; u < units; u += 32) dst[u] = src[u];
+            for (int u = lane; u < units; u += 32) dst[u] = src[u];
+        }
+        __syncthreads();
     }
+    if (all == A.tokens) return;
     // rows behind the last
     const int end = max(BMP, (all + BMP - 1) / BMP * BMP);
     for (int r = all + blockIdx.x * kWarps + warp; r < end; r += gridDim.x * kWarps) {
@@ -936,7 +942,8 @@ cudaError_t launch_rows(const HeadLoss& L, const Layout& l, bool backward, cudaS
     A.tickets = reinterpret_cast<unsigned*>(ws + l.tickets);
     A.ntickets = l.ntickets;
     A.status = L.status;
-    head_rows_kernel<<<static_cast<unsigned>((L.tokens + kRowsPerCta - 1) / kRowsPerCta), kRowsThreads, 0, stream>>>(A);
+    const long long per = align_up((L.tokens + kRowsMostCtas - 1) / kRowsMostCtas, kRowsWarps);
+    head_rows_kernel<<<static_cast<unsigned>((L.tokens + per - 1) / per), kRowsThreads, 0, stream>>>(A, static_cast<int>(per));
     return cudaGetLastError();
 }
 

@@ -378,6 +378,14 @@ def test_head_loss_pieces():
     status_ok()
 
 
+@pytest.mark.parametrize("n", [8200, 33000])
+def test_head_loss_many_tokens(n):
+    """More tokens than one step of the launch that finds the rows, half of them ignored."""
+    check_head(*head_case(n, 300, 64, 92, ignored=0.5))
+    check_head(*head_case(n, 300, 64, 93))
+    status_ok()
+
+
 def test_head_loss_repeats():
     h, w, t, dloss = head_case(1000, 5000, 256, 95, 0.2)
     loss, lse = mo.muon_head_loss(h, w, t)

@@ -2,6 +2,9 @@
 training step through all of them and the hybrid optimizer, row-sparse
 gradients, CUDA graphs, streams, and sizes past 2^31 elements."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -16,6 +19,7 @@ from tests._util import to64
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BF, F32 = torch.bfloat16, torch.float32
 
 
@@ -400,6 +404,31 @@ def test_captured_calls_replay_as_eager(n):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     status_ok()
+
+
+def test_first_call_under_capture_is_refused():
+    """The first call of a process allocates the status word, which no capture
+    allows: it is refused, and the same call works afterwards."""
+    code = """
+import torch, matrix_orthogonalizing_optimizer_step_b200 as mo
+table, t = torch.ones(4, 8, device="cuda"), torch.zeros(3, dtype=torch.long, device="cuda")
+torch.cuda.synchronize()
+try:
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        mo.muon_embedding(t, table)
+except mo.MuonError as e:
+    assert e.code == mo.MUON_ERR_UNSUPPORTED, e
+else:
+    raise SystemExit("not refused")
+assert torch.equal(mo.muon_embedding(t, table), table[t])
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = mo.muon_embedding(t, table)
+g.replay()
+assert torch.equal(out, table[t])
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 def test_two_graphs_replay_at_once():
