@@ -288,7 +288,9 @@ def muon_clear_shape_coeffs():
 
 
 def muon_device_status(device=None):
-    """(status, first bad matrix index or -1); synchronises the bound stream."""
+    """(status, first bad matrix index or -1; for MUON_ERR_INDEX the first
+    position of a token or target outside the vocabulary); synchronises the
+    bound stream."""
     import torch
     _bind_stream(device if device is not None else torch.cuda.current_device())
     bad = ctypes.c_int(-1)
