@@ -47,8 +47,8 @@ namespace {
 // ---- lookup -------------------------------------------------------------------
 
 // A warp copies 1024 columns of one row, four independent 8-element loads per
-// lane: enough in flight at full occupancy (28 registers) for 6.6 TB/s of reads
-// and writes at 65536 x 768, and few rows still spread over several warps.
+// lane: enough in flight at full occupancy (28 registers) for 6 TB/s of reads
+// and writes from cold caches at 65536 x 768, and few rows still spread over several warps.
 constexpr int kFwdWarps = 4;
 constexpr int kSeg = 1024;
 
@@ -725,9 +725,12 @@ cudaError_t launch_class_group(const EmbedBwd& L, int classes, const BwdLayout& 
     A.status = L.status;
     const size_t smem = 4 * static_cast<size_t>(class_list_words(A.count));
     auto kernel = L.out_dt == DT_F32 ? class_group_kernel<float> : class_group_kernel<__nv_bfloat16>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
+    // above the 48 KB that every kernel may use, 13 of them static
+    if (smem > 32 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
     kernel<<<classes, kClassThreads, smem, stream>>>(A);
     return cudaGetLastError();
 }

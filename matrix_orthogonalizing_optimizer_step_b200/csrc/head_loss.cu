@@ -112,7 +112,7 @@ struct HeadGemm {
     CUtensorMap o;      // PROB: P store.                              GRAD: fp32 dh slots
     CUtensorMap o2;     // GRAD: dW store
     const int* nvalid;  // rows that count
-    unsigned* ticket;   // next unclaimed tile
+    unsigned* ticket;   // tiles claimed after the pairs' first ones
     const int* target;  // per copied row
     const float* lse;
     const float* dloss; // per copied row, over *scale
@@ -317,10 +317,10 @@ __device__ void producer(const HeadGemm& L, int nvalid, uint8_t* tiles_smem, Sha
 
 template <int MODE>
 __device__ void scheduler(const HeadGemm& L, int nvalid, Shared* sh) {
-    const uint32_t n = tile_count<MODE>(L, nvalid);
+    const uint32_t n = tile_count<MODE>(L, nvalid), pairs = gridDim.x / 2;
     RingWriter wr;
-    while (true) {
-        const uint32_t t = atomicAdd(L.ticket, 1u);
+    // the first tile of a pair is its own number, without a trip to the counter
+    for (uint32_t t = blockIdx.x / 2;; t = pairs + atomicAdd(L.ticket, 1u)) {
         if (!wr.push(sh, t < n ? t : kEnd, L.wait_ns)) {
             record_timeout(sh, L.status);
             return;
@@ -578,6 +578,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     if (warp == 1) {
         tmem_alloc_pair(&sh->tmem_base, TMEM_COLS);
         tmem_relinquish_pair();
+    }
+    if (warp == 0 && lane == 0) {  // the maps' first use waits for their fetch otherwise
+        tma_prefetch_map(&L.a);
+        tma_prefetch_map(&L.b);
+        tma_prefetch_map(&L.all);
+        if (MODE == GRAD) {
+            tma_prefetch_map(&L.a2);
+            tma_prefetch_map(&L.b2);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -865,10 +874,17 @@ int max_pairs() {
 
 template <int MODE>
 cudaError_t launch_gemm(const HeadGemm& G, long long tiles, cudaStream_t stream) {
-    // the attribute belongs to the device: set on every call, the current one's
-    cudaError_t e = cudaFuncSetAttribute(head_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(SMEM_BYTES));
+    // the attribute belongs to the device: set once on each
+    static bool raised[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= 64 || !raised[dev]) {
+        e = cudaFuncSetAttribute(head_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(SMEM_BYTES));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) raised[dev] = true;
+    }
     const int pairs = max_pairs<MODE>();
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     const unsigned grid = 2 * static_cast<unsigned>(std::min<long long>(pairs, tiles));

@@ -97,6 +97,22 @@ def test_embedding_backward_runs(n):
     status_ok()
 
 
+@pytest.mark.parametrize("n", [100, 3000, 16384])
+def test_embedding_backward_one_class(n):
+    """Tokens that are all equal modulo the SM count, which the first launch
+    gives to one CTA: few and many rows, long and short runs."""
+    sms = torch.cuda.get_device_properties(DEV).multi_processor_count
+    vocab, dim = 40001, 24
+    rows = (vocab - 1) // sms
+    g = torch.randint(-3, 4, (n, dim), generator=gen(8), device=DEV).float()
+    i = torch.arange(n, device=DEV)
+    for t in (i % rows * sms, i * 7 % 5 * sms + 3, torch.where(i % 3 == 0, sms, i % rows * sms)):
+        got = mo.muon_embedding_backward(t, g, vocab)
+        want = torch.zeros(vocab, dim, device=DEV, dtype=torch.float64).index_add_(0, t, g.double())
+        assert torch.equal(got.double(), want)
+    status_ok()
+
+
 def test_embedding_backward_strides_and_out():
     vocab, n = 37, 50
     wide = normal((n, 80), 8, BF)
@@ -209,6 +225,21 @@ def test_layer_norm_strides_shapes_and_special_rows():
     got = mo.muon_layer_norm_backward(dy, x, mean, rstd, w)
     for a, c in zip(got, mo.muon_layer_norm_backward(dy.contiguous(), x.contiguous(), mean, rstd, w)):
         assert torch.equal(a, c)
+    # rows that start on 2 bytes
+    for dim in (64, 333):
+        flat, gflat = normal((5 * dim + 1,), 28, BF), normal((5 * dim + 1,), 29, BF)
+        xb, gb = flat[1:].view(5, dim), gflat[1:].view(5, dim)
+        wb = normal((dim,), 30, F32)
+        one = mo.muon_layer_norm(xb, wb)
+        for a, c in zip(one, mo.muon_layer_norm(xb.clone(), wb)):
+            assert a.shape == c.shape
+        for a, v, e in zip(one, ref.norm(xb, wb, None, 1e-5), ref.norm_bounds(xb, wb, None, 1e-5, BF)):
+            ref.close(a, v, e)
+        got, want = (mo.muon_layer_norm_backward(q, v, one[1], one[2], wb) for q, v in ((gb, xb), (gb.clone(), xb.clone())))
+        v64, e64 = ref.norm_grad(gb, xb, one[1], one[2], wb)
+        for a, c, v, e in zip(got, want, v64, e64):
+            for k in (a, c):
+                ref.close(k, v, e + ref.half(k.dtype) * (v.abs() + e))
     # no rows: empty outputs and zero parameter gradients
     y, mean, rstd = mo.muon_layer_norm(x[:0], w)
     assert y.shape == (0, 3, 64) and mean.shape == (0, 3)
