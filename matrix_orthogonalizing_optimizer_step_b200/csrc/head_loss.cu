@@ -640,7 +640,7 @@ struct RowsArgs {
 
 constexpr int kRowsThreads = 256;
 constexpr int kRowsWarps = kRowsThreads / 32;
-constexpr int kRowsMostCtas = 1024;  // each reads all targets: 8 bytes x tokens x 1024 from L2 at most
+constexpr int kRowsMostCtas = 1024;  // each reads all targets: 8 bytes x tokens x 1024 from L2 at most (148 to 592: no faster)
 
 __device__ __forceinline__ long long target_at(const RowsArgs& A, int t) {
     return A.targets_i64 ? static_cast<const long long*>(A.targets)[t] : static_cast<const int*>(A.targets)[t];
@@ -758,21 +758,36 @@ __global__ void __launch_bounds__(32 * kJoinGroups)
     const int t = blockIdx.x * 32 + lane;
     wait_predecessor();
     const int r = t < tokens ? index[t] : kIgnored;
-    float m = -INFINITY, s = 0.f;
-    auto join = [&](float2 p) {
-        const float top = fmaxf(m, p.x);
-        const float ref = top == -INFINITY ? 0.f : top;
-        s = s * exp_diff(m - ref) + p.y * exp_diff(p.x - ref);
-        m = top;
-    };
+    float m = -INFINITY, s = 0.f;  // several pairs at a time: one maximum, then independent terms
     if (r >= 0) {
-#pragma unroll 4
-        for (int i = g; i < nparts; i += kJoinGroups) join(part[i * row_pitch + r]);
+        constexpr int kAhead = 8;
+        for (int i0 = g; i0 < nparts; i0 += kAhead * kJoinGroups) {
+            float2 p[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int at = i0 + i * kJoinGroups;
+                p[i] = at < nparts ? part[at * row_pitch + r] : make_float2(-INFINITY, 0.f);
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) top = fmaxf(top, p[i].x);
+            const float ref = top == -INFINITY ? 0.f : top;
+            s *= exp_diff(m - ref);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) s += p[i].y * exp_diff(p[i].x - ref);
+            m = top;
+        }
     }
     red[g][lane] = make_float2(m, s);
     __syncthreads();
     if (g != 0 || t >= tokens) return;
-    for (int i = 1; i < kJoinGroups; ++i) join(red[i][lane]);
+    m = -INFINITY;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinGroups; ++i) m = fmaxf(m, red[i][lane].x);
+    const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int i = 0; i < kJoinGroups; ++i) s += red[i][lane].y * exp_diff(red[i][lane].x - ref);
     const float l = m + logf(s);
     const float nan = __int_as_float(0x7fc00000);
     lse[t] = r >= 0 ? l : (r == kBadTarget ? nan : 0.f);
@@ -929,14 +944,22 @@ Layout layout(long long tokens, long long vocab, long long dim, bool backward) {
         l.pieces = (l.vtiles + most - 1) / most;
         l.piece_tiles = (l.vtiles + l.pieces - 1) / l.pieces;
         l.pieces = (l.vtiles + l.piece_tiles - 1) / l.piece_tiles;
-        // K of a dh tile is the piece: cut it where a tile would be more than
-        // a quarter of a pair's share of the launch
+        // K of a dh tile is the piece.  The dh tiles come first and the shorter
+        // dW tiles fill up, so a tile is cut only until the pairs with the most
+        // dh tiles stay below 3/5 of an equal share of the launch: fewer cuts are
+        // fewer fp32 slots to write and add.  (Against 16 to a quarter of a
+        // share: 512 tokens, 50257 x 768 160 instead of 174 us, 2048, 20000 x
+        // 2048 435 instead of 470; 9/10 was 7 % slower at 8192, 50257 x 768,
+        // 9/20, which short batches cannot reach, 15-40 % slower.)
         const long long nd = (dim + BN - 1) / BN, R = l.tpad / BMP, kv = l.piece_tiles * (BN / BK);
-        const long long work = R * nd * kv + l.piece_tiles * nd * (l.tpad / BK);
-        const long long slices = std::min(kv, std::max(16ll, work / kPairsNominal / 4));
+        const long long share = (R * nd * kv + l.piece_tiles * nd * (l.tpad / BK)) / kPairsNominal;
+        long long cuts = 1, slices = kv;
+        while (slices > 16 && (R * nd * cuts + kPairsNominal - 1) / kPairsNominal * slices > share * 3 / 5) {
+            ++cuts;
+            slices = (kv + cuts - 1) / cuts;
+        }
+        l.split_slices = static_cast<int>(slices);
         l.splits = static_cast<int>((kv + slices - 1) / slices);
-        l.split_slices = static_cast<int>((kv + l.splits - 1) / l.splits);
-        l.splits = static_cast<int>((kv + l.split_slices - 1) / l.split_slices);
         l.ntickets = static_cast<int>(2 * l.pieces);
         l.lse = take(4ull * l.tpad);
         l.dloss = take(4ull * l.tpad);

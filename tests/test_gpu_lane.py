@@ -67,7 +67,7 @@ def test_embedding_shapes_and_offsets():
 @pytest.mark.parametrize("n,vocab,dim", [(1, 1, 1), (1, 1000, 8), (16, 3, 40), (17, 1, 333), (300, 7, 264),
                                          (1000, 5003, 333), (4096, 300, 768), (777, 70000, 24),
                                          (16384, 2000, 40), (16385, 900, 72), (20000, 5003, 33),
-                                         (600, 400000, 8)])
+                                         (600, 400000, 8), (70000, 3000, 8), (33000, 400000, 8)])
 def test_embedding_backward(gd, od, n, vocab, dim):
     g = normal((n, dim), 5, gd)
     for it, padding, scale in ((torch.int64, None, 1.0), (torch.int32, vocab // 2, 2.5)):
