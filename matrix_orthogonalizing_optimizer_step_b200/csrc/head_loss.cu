@@ -39,11 +39,16 @@
 // first: their K is the piece, the longest.
 //
 // The tensor cores add into their fp32 accumulator without rounding to
-// nearest, so long sums drift towards zero: the loss is off by 1.3e-6 of its
-// value at dim 768 and 4e-6 at 4096 (a plain fp32 product: 5e-7 and 8e-7).
-// Ending the sum every 768 elements and adding the parts in registers gave
-// 7e-7 at 4096 and cost 9-14 % of the forward product (2946 to 3309 us), which
-// the tolerance of an fp32 loss does not ask for.
+// nearest, so long sums drift towards zero, the large ones most: the targets'
+// logits, which a trained model makes large.  An epilogue warp therefore makes
+// the target's logit of its rows itself, in fp32 with every addition rounded to
+// nearest, while the tile's MMAs run, and puts it in the place of the
+// product's, forward and backward alike.  Losses of targets that lead by 7 are
+// then off by 1e-7 of their value at dim 768 and 1.1e-6 at 4096, where what is
+// left is the drift of the sum of the others (1.3e-6 and 4e-6 with the
+// product's; a plain fp32 product: 5e-7 and 8e-7), for no measurable time.
+// Ending the sums every 768 elements and adding the parts in registers gave
+// 7e-7 at 4096 and cost 9-14 % of the forward product.
 //
 // Measured: loss and gradients of 8192 tokens, 50257 x 768, 2.05-2.19 ms (2.53
 // TFLOP: 1.2 PFLOP/s); 3/4 of 4096 tokens, 128256 x 4096, 9.5-9.8 ms (12.9 TFLOP:
@@ -111,6 +116,10 @@ struct HeadGemm {
     CUtensorMap all;    // the caller's hidden rows as a or b2: read instead where every row counts
     CUtensorMap o;      // PROB: P store.                              GRAD: fp32 dh slots
     CUtensorMap o2;     // GRAD: dW store
+    const __nv_bfloat16* hidden;  // STATS, PROB: the caller's hidden rows, `ldh` apart,
+    const __nv_bfloat16* rows;    // the copied ones, `dim` apart,
+    const __nv_bfloat16* weight;  // and the weight's rows, for the targets' logits
+    long long ldh;
     const int* nvalid;  // rows that count
     unsigned* ticket;   // tiles claimed after the pairs' first ones
     const int* target;  // per copied row
@@ -392,6 +401,60 @@ __device__ void mma_issuer(const HeadGemm& L, int nvalid, uint8_t* tiles_smem, S
     }
 }
 
+// Scalar products of N pairs of rows of 8 * units bf16 values, by a warp:
+// products are exact in fp32, the fused additions and the tree's are rounded to
+// nearest.
+template <int N>
+__device__ __forceinline__ void warp_dot(const __nv_bfloat16* const (&a)[N], const __nv_bfloat16* const (&b)[N],
+                                         int units, int lane, float (&sum)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] = 0.f;
+#pragma unroll(N == 1 ? 4 : 1)
+    for (int u = lane; u < units; u += 32) {
+        uint4 p[N], q[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            p[i] = reinterpret_cast<const uint4*>(a[i])[u];
+            q[i] = reinterpret_cast<const uint4*>(b[i])[u];
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float x[8], y[8];
+            unpack8(p[i], DT_BF16, x);
+            unpack8(q[i], DT_BF16, y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[i] = fmaf(x[j], y[j], sum[i]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+    }
+}
+
+// Takes the N lowest lanes off `here` (at least one; where fewer are left, the
+// last of them again) and makes their rows' target logits.
+template <int N>
+__device__ __forceinline__ void target_logits(const HeadGemm& L, int nvalid, int row0, int y, int lane,
+                                              unsigned& here, float& ly) {
+    int of[N];
+    const __nv_bfloat16 *h[N], *w[N];
+    float l[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        of[i] = __ffs(here) - 1;
+        if (here & (here - 1) || i == N - 1) here &= here - 1;
+        const long long r = row0 + of[i], v = L.v0 + __shfl_sync(0xffffffffu, y, of[i]);
+        h[i] = nvalid == L.tokens ? L.hidden + r * L.ldh : L.rows + r * L.dim;
+        w[i] = L.weight + v * L.dim;
+    }
+    warp_dot<N>(h, w, L.dim / 8, lane, l);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (lane == of[i]) ly = l[i];
+}
+
 template <int MODE>
 __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32_t stg, uint32_t tmem_base, int warp,
                                int lane, uint32_t rank) {
@@ -438,7 +501,7 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
         const int row0 = x.m0 + static_cast<int>(rank) * BM + q * 32, row = row0 + lane;
         const int cbase = x.n0 + part * PART_COLS;
         int y = -1;
-        float lse = 0.f, dl = 0.f;
+        float lse = 0.f, dl = 0.f, ly = 0.f;
         if (MODE != GRAD) {
             if (row < nvalid) {
                 y = L.target[row] - L.v0;  // column of the target in this piece
@@ -446,6 +509,14 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
                     lse = L.lse[row];
                     dl = L.dloss[row];
                 }
+            }
+            // the targets' logits of the rows that have theirs in these columns
+            unsigned here = __ballot_sync(0xffffffffu, y >= cbase && y < cbase + PART_COLS);
+            while (here) {
+                if (here & (here - 1))
+                    target_logits<4>(L, nvalid, row0, y, lane, here, ly);
+                else
+                    target_logits<1>(L, nvalid, row0, y, lane, here, ly);
             }
         }
         const bool got = mbar_wait(&sh->tfull[acc], acc_phase, abort_flag, lim);
@@ -471,11 +542,10 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
             if (MODE == STATS) {
                 const int at = y - col0;
                 if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
-                    float l = 0.f;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (j == at) l = v[j];
-                    if (at >= 0 && at < 32) L.tlogit[row] = l;
+                        if (j == at) v[j] = ly;
+                    if (at >= 0 && at < 32) L.tlogit[row] = ly;
                 }
                 if (ncols < 32) {
 #pragma unroll
@@ -496,10 +566,10 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = dl * exp_diff(v[j] - lse);
                 if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
-                    float g = 0.f;
+                    const float g = dl * exp_diff(ly - lse) - dl;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (j == at) g = v[j] -= dl;
+                        if (j == at) v[j] = g;
                     if (at >= 0 && at < 32) L.rest[row] = g - __bfloat162float(__float2bfloat16_rn(g));
                 }
                 // rows behind the last that counts and columns behind the
@@ -788,10 +858,13 @@ __global__ void __launch_bounds__(32 * kJoinGroups)
     const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int i = 0; i < kJoinGroups; ++i) s += red[i][lane].y * exp_diff(red[i][lane].x - ref);
-    const float l = m + logf(s);
-    const float nan = __int_as_float(0x7fc00000);
-    lse[t] = r >= 0 ? l : (r == kBadTarget ? nan : 0.f);
-    loss[t] = r >= 0 ? l - tlogit[r] : (r == kBadTarget ? nan : 0.f);
+    // the maximum is at least the target's logit and the sum at least its share,
+    // so a loss made of their differences keeps its digits where it is small and
+    // is never negative
+    const float log_sum = logf(s);
+    const float none = r == kBadTarget ? __int_as_float(0x7fc00000) : 0.f;
+    lse[t] = r >= 0 ? m + log_sum : none;
+    loss[t] = r >= 0 ? (m - tlogit[r]) + log_sum : none;
 }
 
 // dh: the sum of a row's slots and what rounding took off the target's entry,
@@ -1008,6 +1081,10 @@ HeadGemm gemm_args(const HeadLoss& L, const Layout& l) {
     HeadGemm G{};
     G.nvalid = reinterpret_cast<const int*>(ws + l.nvalid);
     G.target = reinterpret_cast<const int*>(ws + l.target);
+    G.hidden = static_cast<const __nv_bfloat16*>(L.hidden);
+    G.rows = reinterpret_cast<const __nv_bfloat16*>(ws + l.rows);
+    G.weight = static_cast<const __nv_bfloat16*>(L.weight);
+    G.ldh = L.ldh;
     G.vocab = static_cast<int>(L.vocab);
     G.dim = static_cast<int>(L.dim);
     G.tokens = static_cast<int>(L.tokens);

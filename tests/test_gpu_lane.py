@@ -425,3 +425,38 @@ def test_head_loss_repeats():
     for a, c in zip(first, (loss, lse, *mo.muon_head_loss_backward(h, w, t, lse, dloss))):
         assert torch.equal(a, c)
     status_ok()
+
+
+@pytest.mark.parametrize("ignored", [0.0, 0.3])
+def test_head_loss_equal_targets(ignored):
+    # one token is every row's target, then a few tokens of one 128-column stretch are
+    h, w, t, dloss = head_case(300, 1500, 264, 96, ignored)
+    counts = t != -100
+    t[counts] = 777
+    check_head(h, w, t, dloss)
+    t[counts] = 640 + torch.arange(int(counts.sum()), device=DEV) % 5
+    check_head(h, w, t, dloss)
+
+
+def test_head_loss_of_confident_rows():
+    # the target's logit leads by 8 to 40: losses from 0.5 down to 1e-14
+    n, vocab, dim = 300, 5003, 2048
+    g = torch.Generator(device=DEV).manual_seed(97)
+    w = (torch.randn(vocab, dim, generator=g, device=DEV) * 0.02).bfloat16()
+    t = torch.randint(0, vocab, (n,), generator=g, device=DEV)
+    lead = torch.linspace(8, 40, n, device=DEV)[:, None]
+    wt = w[t].float()
+    h = (torch.randn(n, dim, generator=g, device=DEV) * 0.1 + wt * (lead / wt.square().sum(1, keepdim=True))).bfloat16()
+    loss, lse = mo.muon_head_loss(h, w, t)
+    vloss, vlse, p, valid, h64, at = ref.head(h, w, t, -100)
+    assert (h64 @ w.double().T).argmax(1).eq(t).all()
+    # log s of s = 1 + x: the maximum is the target's logit itself.  x is off by
+    # the logits' differences' error and the exponential's, and s by half a step
+    # for each addition to a sum that holds the 1: 128 columns, the pairs of a
+    # group (each scaled), 32 groups; log by 2 steps
+    _, _, el = ref.head_bounds(h64, w, vlse, valid)
+    x = torch.expm1(vloss)
+    additions = 128 + 2 * (vocab / 4096 + 1) + 2 * 32
+    ref.close(loss, vloss, x * (torch.expm1(2 * el) + 2.0 ** -19) + additions * ref.U + 4 * ref.U * vloss)
+    assert (loss >= 0).all()
+    assert loss[-1] < 1e-6
