@@ -708,9 +708,9 @@ struct RowsArgs {
     DeviceStatus* status;
 };
 
-constexpr int kRowsThreads = 256;
+constexpr int kRowsThreads = 1024;
 constexpr int kRowsWarps = kRowsThreads / 32;
-constexpr int kRowsMostCtas = 1024;  // each reads all targets: 8 bytes x tokens x 1024 from L2 at most (148 to 592: no faster)
+constexpr int kRowsMostCtas = 256;  // each reads all targets: two CTAs per SM, 8 bytes x tokens x 256 from L2
 
 __device__ __forceinline__ long long target_at(const RowsArgs& A, int t) {
     return A.targets_i64 ? static_cast<const long long*>(A.targets)[t] : static_cast<const int*>(A.targets)[t];
@@ -721,13 +721,14 @@ __device__ __forceinline__ bool counts(const RowsArgs& A, long long y) {
 
 // Finds the place of every row that counts among those that do and, if some do
 // not, copies the ones that do together, in order; the copied rows up to the
-// next multiple of 256 are zeroed.  A CTA has `per` tokens (a multiple of 8)
-// and counts all targets before them itself.
+// next multiple of 256 are zeroed.  A CTA has `per` tokens and counts all
+// targets before them itself: 1024 threads, so that this is a trip or two to L2
+// (8192 tokens: 8 us forward, 9 backward; 256 threads in 1024 CTAs 12 and 17).
 __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs A, int per) {
-    constexpr int kWarps = kRowsWarps;
-    __shared__ int red[2][kWarps];
-    __shared__ float red_dl[kWarps];
-    __shared__ int dst_of[32];
+    __shared__ int red[2][kRowsWarps];
+    __shared__ float red_dl[kRowsWarps];
+    __shared__ int warp_n[kRowsWarps];
+    __shared__ int dst_of[kRowsThreads];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     allow_successor();
     const int t0 = blockIdx.x * per, t1 = min(t0 + per, A.tokens);
@@ -740,24 +741,21 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs 
         if (t < t0) before += c ? 1 : 0;
         if (A.dloss_in && c) top = fmaxf(top, fabsf(A.dloss_in[t]));
     }
+    before = __reduce_add_sync(0xffffffffu, before);
+    all = __reduce_add_sync(0xffffffffu, all);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) {
         red[0][warp] = before;
         red[1][warp] = all;
         red_dl[warp] = top;
     }
     __syncthreads();
-    before = all = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        before += red[0][w];
-        all += red[1][w];
-        top = fmaxf(top, red_dl[w]);
-    }
+    before = __reduce_add_sync(0xffffffffu, red[0][lane]);
+    all = __reduce_add_sync(0xffffffffu, red[1][lane]);
+    top = red_dl[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     // the common factor of dloss; 1 where it would not be one
     const float scale = top > 0.f && top <= 3.4e38f ? top : 1.f;
     if (blockIdx.x == 0) {
@@ -768,35 +766,36 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs 
         for (int i = tid; i < A.ntickets; i += kRowsThreads) A.tickets[i] = 0;
     }
     const int units = A.dim / 8;  // 16-byte units of a row
-    for (int s0 = t0; s0 < t1; s0 += 32) {
-        if (warp == 0) {
-            const int t = s0 + lane;
-            const bool in = t < t1;
-            const long long y = in ? target_at(A, t) : A.ignore;
-            const bool on = in && counts(A, y);
-            const unsigned mask = __ballot_sync(0xffffffffu, on);
-            const int r = before + __popc(mask & ((1u << lane) - 1));
-            dst_of[lane] = on ? r : -1;
-            before += __popc(mask);
-            if (on) {
-                A.target[r] = static_cast<int>(y);
-                if (A.dloss_in) {
-                    A.lse[r] = A.lse_in[t];
-                    A.dloss[r] = A.dloss_in[t] / scale;
-                }
-            }
-            if (in) {
-                const bool bad = !on && y != A.ignore;
-                A.index[t] = on ? r : (bad ? kBadTarget : kIgnored);
-                if (bad) {
-                    atomicMin(&A.status->first_bad_token, t);
-                    atomicOr(&A.status->bits, ST_INDEX);
-                }
+    for (int s0 = t0; s0 < t1; s0 += kRowsThreads) {
+        const int t = s0 + tid;
+        const bool in = t < t1;
+        const long long y = in ? target_at(A, t) : A.ignore;
+        const bool on = in && counts(A, y);
+        const unsigned mask = __ballot_sync(0xffffffffu, on);
+        if (lane == 0) warp_n[warp] = __popc(mask);
+        __syncthreads();
+        const int n = warp_n[lane];
+        const int r = before + __reduce_add_sync(0xffffffffu, lane < warp ? n : 0) + __popc(mask & ((1u << lane) - 1));
+        before += __reduce_add_sync(0xffffffffu, n);
+        dst_of[tid] = on ? r : -1;
+        if (on) {
+            A.target[r] = static_cast<int>(y);
+            if (A.dloss_in) {
+                A.lse[r] = A.lse_in[t];
+                A.dloss[r] = A.dloss_in[t] / scale;
             }
         }
-        if (all == A.tokens) continue;  // the products read the caller's rows
+        if (in) {
+            const bool bad = !on && y != A.ignore;
+            A.index[t] = on ? r : (bad ? kBadTarget : kIgnored);
+            if (bad) {
+                atomicMin(&A.status->first_bad_token, t);
+                atomicOr(&A.status->bits, ST_INDEX);
+            }
+        }
         __syncthreads();
-        for (int i = warp; i < min(32, t1 - s0); i += kWarps) {
+        if (all == A.tokens) continue;  // the products read the caller's rows
+        for (int i = warp; i < min(kRowsThreads, t1 - s0); i += kRowsWarps) {
             if (dst_of[i] < 0) continue;
             const uint4* src = reinterpret_cast<const uint4*>(A.hidden + (s0 + i) * A.ldh);
             uint4* dst = reinterpret_cast<uint4*>(A.rows + static_cast<long long>(dst_of[i]) * A.dim);
@@ -808,7 +807,7 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs 
     if (all == A.tokens) return;
     // rows behind the last
     const int end = max(BMP, (all + BMP - 1) / BMP * BMP);
-    for (int r = all + blockIdx.x * kWarps + warp; r < end; r += gridDim.x * kWarps) {
+    for (int r = all + blockIdx.x * kRowsWarps + warp; r < end; r += gridDim.x * kRowsWarps) {
         uint4* dst = reinterpret_cast<uint4*>(A.rows + static_cast<long long>(r) * A.dim);
         for (int u = lane; u < units; u += 32) dst[u] = make_uint4(0, 0, 0, 0);
     }
@@ -816,27 +815,38 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs 
 
 // ---- joins -----------------------------------------------------------------------
 
-constexpr int kJoinGroups = 32;
+constexpr int kJoinWarps = 32;
 
-// One CTA per 32 tokens: group g joins the (max, sum) pairs g, g + 32, ... of
-// each row, then the groups' pairs are joined in order.
-__global__ void __launch_bounds__(32 * kJoinGroups)
+// (max, sum) pairs as one: the sum of s exp(m - max).
+__device__ __forceinline__ float2 join_pairs(float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x), ref = m == -INFINITY ? 0.f : m;
+    return make_float2(m, a.y * exp_diff(a.x - ref) + b.y * exp_diff(b.x - ref));
+}
+
+// A CTA joins the (max, sum) pairs of TOKENS tokens (8 or 32): group g of G takes
+// the pairs g, g + G, ... of a token, eight loads in flight; then the groups'
+// pairs are joined in a fixed order.  8 tokens are 128 groups, one trip to
+// memory for a vocabulary of 131072, and more CTAs; 32 tokens read whole lines.
+template <int TOKENS>
+__global__ void __launch_bounds__(32 * kJoinWarps)
     head_join_kernel(const float2* part, int nparts, long long row_pitch, const float* tlogit, const int* index,
                      int tokens, float* loss, float* lse) {
-    __shared__ float2 red[kJoinGroups][33];
-    const int lane = threadIdx.x % 32, g = threadIdx.x / 32;
-    const int t = blockIdx.x * 32 + lane;
+    constexpr int kPerWarp = 32 / TOKENS, kGroups = kPerWarp * kJoinWarps;
+    __shared__ float2 red[kJoinWarps][TOKENS];
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int at = lane % TOKENS, g = warp * kPerWarp + lane / TOKENS;
+    const int t = blockIdx.x * TOKENS + at;
     wait_predecessor();
     const int r = t < tokens ? index[t] : kIgnored;
     float m = -INFINITY, s = 0.f;  // several pairs at a time: one maximum, then independent terms
     if (r >= 0) {
         constexpr int kAhead = 8;
-        for (int i0 = g; i0 < nparts; i0 += kAhead * kJoinGroups) {
+        for (int i0 = g; i0 < nparts; i0 += kAhead * kGroups) {
             float2 p[kAhead];
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const int at = i0 + i * kJoinGroups;
-                p[i] = at < nparts ? part[at * row_pitch + r] : make_float2(-INFINITY, 0.f);
+                const int k = i0 + i * kGroups;
+                p[i] = k < nparts ? part[k * row_pitch + r] : make_float2(-INFINITY, 0.f);
             }
             float top = m;
 #pragma unroll
@@ -848,16 +858,27 @@ __global__ void __launch_bounds__(32 * kJoinGroups)
             m = top;
         }
     }
-    red[g][lane] = make_float2(m, s);
+    float2 v = make_float2(m, s);
+#pragma unroll
+    for (int o = TOKENS; o < 32; o <<= 1) {
+        const float2 w = make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
+        v = join_pairs(v, w);
+    }
+    if (lane < TOKENS) red[warp][at] = v;
     __syncthreads();
-    if (g != 0 || t >= tokens) return;
-    m = -INFINITY;
-    s = 0.f;
+    if (warp != 0) return;
+    // of each token's warps' pairs every kPerWarp-th to a lane, then the lanes'
+    v = red[lane / TOKENS][at];
 #pragma unroll
-    for (int i = 0; i < kJoinGroups; ++i) m = fmaxf(m, red[i][lane].x);
-    const float ref = m == -INFINITY ? 0.f : m;
+    for (int i = kPerWarp; i < kJoinWarps; i += kPerWarp) v = join_pairs(v, red[i + lane / TOKENS][at]);
 #pragma unroll
-    for (int i = 0; i < kJoinGroups; ++i) s += red[i][lane].y * exp_diff(red[i][lane].x - ref);
+    for (int o = TOKENS; o < 32; o <<= 1) {
+        const float2 w = make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
+        v = join_pairs(v, w);
+    }
+    if (lane >= TOKENS || t >= tokens) return;
+    m = v.x;
+    s = v.y;
     // the maximum is at least the target's logit and the sum at least its share,
     // so a loss made of their differences keeps its digits where it is small and
     // is never negative
@@ -869,6 +890,8 @@ __global__ void __launch_bounds__(32 * kJoinGroups)
 
 // dh: the sum of a row's slots and what rounding took off the target's entry,
 // times the common factor, rounded to bf16; zero for tokens that take no part.
+// AHEAD: slots whose loads are in flight at once.
+template <int AHEAD>
 __global__ void __launch_bounds__(128)
     head_dhidden_kernel(const float* slots, int nslots, long long slot_pitch, const int* index, const int* target,
                         const float* rest, const float* scale, const __nv_bfloat16* weight, int dim,
@@ -884,14 +907,25 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = 0.f;
         if (r >= 0) {
+            const uint4 wc = *reinterpret_cast<const uint4*>(w + c);
             const float* src = slots + static_cast<long long>(r) * dim + c;
-            for (int s = 0; s < nslots; ++s, src += slot_pitch) {
-                const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
-                v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-                v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+            for (int s0 = 0; s0 < nslots; s0 += AHEAD) {
+                float4 a[AHEAD], b[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    if (s0 + i >= nslots) break;
+                    a[i] = *reinterpret_cast<const float4*>(src + (s0 + i) * slot_pitch);
+                    b[i] = *reinterpret_cast<const float4*>(src + (s0 + i) * slot_pitch + 4);
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    if (s0 + i >= nslots) break;
+                    v[0] += a[i].x, v[1] += a[i].y, v[2] += a[i].z, v[3] += a[i].w;
+                    v[4] += b[i].x, v[5] += b[i].y, v[6] += b[i].z, v[7] += b[i].w;
+                }
             }
             float x[8];
-            unpack8(*reinterpret_cast<const uint4*>(w + c), DT_BF16, x);
+            unpack8(wc, DT_BF16, x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] = f * fmaf(d, x[j], v[j]);
         }
@@ -1071,7 +1105,7 @@ cudaError_t launch_rows(const HeadLoss& L, const Layout& l, bool backward, cudaS
     A.tickets = reinterpret_cast<unsigned*>(ws + l.tickets);
     A.ntickets = l.ntickets;
     A.status = L.status;
-    const long long per = align_up((L.tokens + kRowsMostCtas - 1) / kRowsMostCtas, kRowsWarps);
+    const long long per = align_up((L.tokens + kRowsMostCtas - 1) / kRowsMostCtas, 32);
     head_rows_kernel<<<static_cast<unsigned>((L.tokens + per - 1) / per), kRowsThreads, 0, stream>>>(A, static_cast<int>(per));
     return cudaGetLastError();
 }
@@ -1124,8 +1158,12 @@ cudaError_t launch_head_loss(const HeadLoss& L, cudaStream_t stream, int* launch
     if (e != cudaSuccess) return e;
     const int nparts = static_cast<int>((L.vocab + PART_COLS - 1) / PART_COLS);
     *launches += 3;
-    return launch_dependent(head_join_kernel, dim3(static_cast<unsigned>((L.tokens + 31) / 32)), 32 * kJoinGroups, 0,
-                            stream, G.part, nparts, l.tpad, G.tlogit, reinterpret_cast<const int*>(ws + l.index),
+    // 8 tokens per CTA against 32: 256 tokens of 128256 4.6 instead of 8.6 us, 512 of
+    // 50257 3.1 instead of 4.2, 2048 of 20000 6.7 instead of 3.9
+    const int per = L.tokens <= 1024 ? 8 : 32;
+    return launch_dependent(per == 8 ? head_join_kernel<8> : head_join_kernel<32>,
+                            dim3(static_cast<unsigned>((L.tokens + per - 1) / per)), 32 * kJoinWarps, 0, stream, G.part,
+                            nparts, l.tpad, G.tlogit, reinterpret_cast<const int*>(ws + l.index),
                             static_cast<int>(L.tokens), L.loss, L.lse);
 }
 
@@ -1181,7 +1219,10 @@ cudaError_t launch_head_loss_backward(const HeadLoss& L, cudaStream_t stream, in
     }
     if (!L.dhidden) return cudaSuccess;
     ++*launches;
-    return launch_dependent(head_dhidden_kernel, dim3(static_cast<unsigned>(L.tokens)), 128, 0, stream,
+    // one slot per token wants many CTAs on an SM (40 registers), many slots want
+    // loads in flight (200 tokens, 30000 x 1000: 6 instead of 13 us; 8192 tokens of
+    // one slot of 768: 18 instead of 30 us)
+    return launch_dependent(l.splits < 4 ? head_dhidden_kernel<1> : head_dhidden_kernel<8>, dim3(static_cast<unsigned>(L.tokens)), 128, 0, stream,
                             reinterpret_cast<const float*>(ws + l.slots), l.splits, l.tpad * L.dim,
                             reinterpret_cast<const int*>(ws + l.index), reinterpret_cast<const int*>(ws + l.target),
                             P.rest, D.scale, static_cast<const __nv_bfloat16*>(L.weight), static_cast<int>(L.dim),
