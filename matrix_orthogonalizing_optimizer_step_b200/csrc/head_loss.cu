@@ -28,8 +28,8 @@
 //
 // The products use CTA pairs (tcgen05 cta_group::2, M = 256, N = 256, K = 16,
 // bf16 operands, fp32 accumulation in tensor memory) fed by TMA:
-//   warp 10     claims tiles from a counter (leader CTA) and publishes them to
-//               both CTAs through a ring in shared memory
+//   warp 10     claims a pair's tiles but the first from a counter (leader CTA)
+//               and publishes them to both CTAs through a ring in shared memory
 //   warp 0      TMA producer: 64-wide K slices into a 5-stage ring
 //   warp 1      tensor memory owner, MMA issuer (leader CTA)
 //   warps 2..9  epilogue; two accumulators, so it overlaps the next tile
@@ -208,6 +208,14 @@ __device__ __forceinline__ Tile tile_at(const HeadGemm& L, int nvalid, uint32_t 
     return x;
 }
 
+// The first tile of a pair is its own number: all its warps know it without the
+// scheduler.
+template <int MODE>
+__device__ __forceinline__ uint32_t first_tile(const HeadGemm& L, int nvalid) {
+    const uint32_t t = blockIdx.x / 2;
+    return t < tile_count<MODE>(L, nvalid) ? t : kEnd;
+}
+
 __device__ __forceinline__ void record_timeout(Shared* sh, DeviceStatus* st) {
     atomicOr(&st->bits, ST_TIMEOUT);
     *reinterpret_cast<volatile int*>(&sh->abort) = 1;
@@ -266,16 +274,10 @@ __device__ void producer(const HeadGemm& L, int nvalid, uint8_t* tiles_smem, Sha
     const bool leader = rank == 0;
     const CUtensorMap* hidden = nvalid == L.tokens ? &L.all : (MODE == GRAD ? &L.b2 : &L.a);
     int stage = 0;
-    uint32_t phase = 0, issued = 0;
+    uint32_t phase = 0, issued = 0, t = first_tile<MODE>(L, nvalid);
     bool ok = true;
     RingReader rd;
-    while (ok) {
-        uint32_t t;
-        if (!rd.pop(sh, t, leader, lim)) {
-            ok = false;
-            break;
-        }
-        if (t == kEnd) break;
+    while (ok && t != kEnd) {
         const Tile x = tile_at<MODE>(L, nvalid, t);
         const int arow = x.m0 + static_cast<int>(rank) * BM, brow = x.n0 + static_cast<int>(rank) * BNH;
         for (int i = 0; i < x.nk; ++i) {
@@ -310,6 +312,7 @@ __device__ void producer(const HeadGemm& L, int nvalid, uint8_t* tiles_smem, Sha
                 phase ^= 1u;
             }
         }
+        if (ok) ok = rd.pop(sh, t, leader, lim);
     }
     if (!ok) record_timeout(sh, L.status);
     // the last fills of every stage must have landed before the pair exits
@@ -328,8 +331,9 @@ template <int MODE>
 __device__ void scheduler(const HeadGemm& L, int nvalid, Shared* sh) {
     const uint32_t n = tile_count<MODE>(L, nvalid), pairs = gridDim.x / 2;
     RingWriter wr;
-    // the first tile of a pair is its own number, without a trip to the counter
-    for (uint32_t t = blockIdx.x / 2;; t = pairs + atomicAdd(L.ticket, 1u)) {
+    if (first_tile<MODE>(L, nvalid) == kEnd) return;
+    while (true) {
+        const uint32_t t = pairs + atomicAdd(L.ticket, 1u);
         if (!wr.push(sh, t < n ? t : kEnd, L.wait_ns)) {
             record_timeout(sh, L.status);
             return;
@@ -343,17 +347,11 @@ __device__ void mma_issuer(const HeadGemm& L, int nvalid, uint8_t* tiles_smem, S
     volatile int* abort_flag = &sh->abort;
     const unsigned long long lim = L.wait_ns;
     int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
+    uint32_t phase = 0, acc_phase = 0, t = first_tile<MODE>(L, nvalid);
     bool ok = true, issued_any = false;
     const uint32_t tiles_base = smem_u32(tiles_smem);
     RingReader rd;
-    while (ok) {
-        uint32_t t;
-        if (!rd.pop(sh, t, true, lim)) {
-            ok = false;
-            break;
-        }
-        if (t == kEnd) break;
+    while (ok && t != kEnd) {
         const Tile x = tile_at<MODE>(L, nvalid, t);
         const int a_mn = MODE == GRAD && x.dw, b_mn = MODE == GRAD;
         const uint32_t idesc = make_instr_desc(1, a_mn, b_mn, BMP, BN);
@@ -390,6 +388,7 @@ __device__ void mma_issuer(const HeadGemm& L, int nvalid, uint8_t* tiles_smem, S
         umma_commit_pair(&sh->tfull[acc], 0x3);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
+        ok = rd.pop(sh, t, true, lim);
     }
     if (!ok) {
         record_timeout(sh, L.status);
@@ -487,16 +486,8 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
         }
         ++nstored;
     };
-    while (true) {
-        uint32_t t = 0;
-        int got_tile = 1;
-        if (lane == 0) got_tile = rd.pop(sh, t, rank == 0, lim) ? 1 : 0;
-        if (!__shfl_sync(0xffffffffu, got_tile, 0)) {
-            if (lane == 0) record_timeout(sh, L.status);
-            break;
-        }
-        t = __shfl_sync(0xffffffffu, t, 0);
-        if (t == kEnd) break;
+    uint32_t t = first_tile<MODE>(L, nvalid);
+    while (t != kEnd) {
         const Tile x = tile_at<MODE>(L, nvalid, t);
         const int row0 = x.m0 + static_cast<int>(rank) * BM + q * 32, row = row0 + lane;
         const int cbase = x.n0 + part * PART_COLS;
@@ -552,14 +543,17 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
                     for (int j = 0; j < 32; ++j)
                         if (j >= ncols) v[j] = -INFINITY;
                 }
-                float top = m;
+                // four chains of each kind
+                float t4[4] = {m, v[1], v[2], v[3]};
 #pragma unroll
-                for (int j = 0; j < 32; ++j) top = fmaxf(top, v[j]);
+                for (int j = 0; j < 32; ++j) t4[j % 4] = fmaxf(t4[j % 4], v[j]);
+                const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                 // all terms so far are zero: any finite reference will do
                 const float ref = top == -INFINITY ? 0.f : top;
-                s *= exp_diff(m - ref);
+                float s4[4] = {s * exp_diff(m - ref), 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s += exp_diff(v[j] - ref);
+                for (int j = 0; j < 32; ++j) s4[j % 4] += exp_diff(v[j] - ref);
+                s = (s4[0] + s4[1]) + (s4[2] + s4[3]);
                 m = top;
             } else if (MODE == PROB) {
                 const int at = y - col0;
@@ -611,6 +605,13 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
         if (MODE == STATS) L.part[static_cast<long long>(cbase / PART_COLS) * L.row_pitch + row] = make_float2(m, s);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
+        int got_tile = 1;
+        if (lane == 0) got_tile = rd.pop(sh, t, rank == 0, lim) ? 1 : 0;
+        if (!__shfl_sync(0xffffffffu, got_tile, 0)) {
+            if (lane == 0) record_timeout(sh, L.status);
+            break;
+        }
+        t = __shfl_sync(0xffffffffu, t, 0);
     }
     if (lane == 0) bulk_wait_all();  // the staging boxes stay valid until every store has read them
     __syncwarp();
