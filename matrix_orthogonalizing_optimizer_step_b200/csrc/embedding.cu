@@ -64,10 +64,11 @@ __device__ __forceinline__ void report_bad_token(DeviceStatus* st, long long t) 
 template <typename TT, typename TO, bool VEC>
 __global__ void __launch_bounds__(kFwdWarps * 32) embedding_kernel(const EmbedFwd L, int nseg) {
     const int lane = threadIdx.x % 32;
-    const long long item = static_cast<long long>(blockIdx.x) * kFwdWarps + threadIdx.x / 32;
-    const long long t = item / nseg;
+    // a CTA has one segment of 4 tokens (32-bit division: a 64-bit one is a call)
+    const unsigned group = blockIdx.x / static_cast<unsigned>(nseg);
+    const long long t = static_cast<long long>(group) * kFwdWarps + threadIdx.x / 32;
     if (t >= L.count) return;
-    const int seg = static_cast<int>(item - t * nseg);
+    const int seg = static_cast<int>(blockIdx.x - group * nseg);
     const long long c0 = static_cast<long long>(seg) * kSeg;
     const long long id = token_at(L.tokens, L.tokens_i64, t);
     const bool bad = id < 0 || id >= L.vocab;
@@ -537,13 +538,14 @@ __device__ __forceinline__ unsigned chunks_of_run(const RunArgs& R, unsigned chu
 template <typename TG, typename TO, bool VEC>
 __global__ void __launch_bounds__(kRunWarps * 32) run_sum_kernel(const RunArgs R) {
     const int lane = threadIdx.x % 32;
-    const long long item = static_cast<long long>(blockIdx.x) * kRunWarps + threadIdx.x / 32;
-    const long long chunk = item / R.nslab;
+    // a CTA has one slab of 4 chunks
+    const unsigned group = blockIdx.x / static_cast<unsigned>(R.nslab);
+    const int slab = static_cast<int>(blockIdx.x - group * R.nslab);
+    const long long chunk = static_cast<long long>(group) * kRunWarps + threadIdx.x / 32;
     const unsigned p0 = static_cast<unsigned>(chunk) * kChunk;
     wait_predecessor();
     if (chunk * kChunk >= R.count) return;
     const int n = min(static_cast<unsigned>(kChunk), R.count - p0);
-    const int slab = static_cast<int>(item - chunk * R.nslab);
     const long long c0 = slab * 256ll;
     // lane i < n: pair i; lane 30: the key before the chunk; lane 31: the key after it
     unsigned k = R.vocab, q = 0;
@@ -779,7 +781,7 @@ cudaError_t launch_run_sum(const RunArgs& R, bool vec, unsigned blocks, cudaStre
 
 cudaError_t launch_embedding(const EmbedFwd& L, cudaStream_t stream) {
     const int nseg = static_cast<int>((L.dim + kSeg - 1) / kSeg);
-    const unsigned blocks = static_cast<unsigned>((L.count * nseg + kFwdWarps - 1) / kFwdWarps);
+    const unsigned blocks = static_cast<unsigned>((L.count + kFwdWarps - 1) / kFwdWarps * nseg);
     const bool vec = rows_vec_ok(L.table, L.dim, L.table_dt) && rows_vec_ok(L.out, L.dim, L.out_dt) && L.dim % 8 == 0;
     auto go = [&](auto tt, auto to) {
         using TT = decltype(tt);
@@ -825,7 +827,7 @@ cudaError_t launch_embedding_backward(const EmbedBwd& L, int num_sms, cudaStream
     R.partial = reinterpret_cast<float*>(ws + lay.partial);
     R.done = reinterpret_cast<unsigned*>(ws + lay.done);
     R.nslab = static_cast<int>((L.dim + 255) / 256);
-    const unsigned blocks = static_cast<unsigned>((lay.ndone + kRunWarps - 1) / kRunWarps);
+    const unsigned blocks = static_cast<unsigned>((lay.chunks + kRunWarps - 1) / kRunWarps * R.nslab);
     const bool vec = rows_vec_ok(L.grad, L.ld, L.grad_dt) && rows_vec_ok(L.out, L.dim, L.out_dt) && L.dim % 8 == 0;
     ++*launches;
     if (L.grad_dt == DT_F32)

@@ -113,7 +113,7 @@ int muon_embedding(const void* tokens, int token_dtype, long long count, const v
     if (!table || !out) return invalid("table and out must not be NULL");
     if (!aligned(table, elem_size(table_dtype)) || !aligned(out, elem_size(out_dtype)))
         return invalid("table and out must be aligned to their type");
-    if (count * ((dim + 1023) / 1024) / 4 >= kMaxGrid) return invalid("count x dim too large for one call");
+    if ((count + 3) / 4 * ((dim + 1023) / 1024) >= kMaxGrid) return invalid("count x dim too large for one call");
     Device dev;
     st = abi_device(&dev.status, &dev.num_sms, &dev.cc_major);
     if (st != MUON_OK) return st;
@@ -153,7 +153,7 @@ int muon_embedding_backward(const void* tokens, int token_dtype, long long count
     if (count > 0 && (!grad_out || !aligned(grad_out, elem_size(grad_dtype))))
         return invalid("grad_out must be aligned to its type and not NULL");
     if (ld_grad < dim) return invalid("ld_grad must be >= dim");
-    if ((count + 15) / 16 * ((dim + 255) / 256) / 4 >= kMaxGrid) return invalid("count x dim too large for one call");
+    if ((count + 63) / 64 * ((dim + 255) / 256) >= kMaxGrid) return invalid("count x dim too large for one call");
     st = workspace_check(workspace, workspace_bytes, embedding_backward_workspace(count, dim));
     if (st != MUON_OK) return st;
     Device dev;

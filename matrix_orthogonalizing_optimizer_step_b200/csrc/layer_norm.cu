@@ -22,9 +22,9 @@
 // Statistics and sums are fp32; outputs are rounded once.
 //
 // Measured (bf16): forward 16384 x 4096 48-51 us (268 MB: 5.2-5.6 TB/s), 16 x 4096
-// 2.7 us on the GPU; backward 16384 x 768 with fp32 parameters 19-20.6 us (75 MB,
+// 2.7 us on the GPU; backward 16384 x 768 with fp32 parameters 18.5 us (75 MB,
 // 11.7 us at the copy rate: rows' chains of latencies and the second launch),
-// 4099 x 1025 fp32 20.5 us (50 MB, 7.8 us: 4-byte copies, and a third of the
+// 4099 x 1025 fp32 18.5 us (50 MB, 7.8 us: 4-byte copies, and a third of the
 // rows' 1536 places empty).
 #include "lane.h"
 #include "pdl.h"
@@ -557,9 +557,24 @@ __global__ void __launch_bounds__(kSumWarps * 32)
     const long long c = static_cast<long long>(blockIdx.x) * 32 + lane;
     float s = 0.f;
     if (c < dim) {
-        const float* p = part + blockIdx.y * dim + c;
-#pragma unroll 8
-        for (int i = warp; i < nparts; i += kSumWarps) s += p[static_cast<long long>(i) * 2 * dim];
+        const float* p = part + (2ll * warp + blockIdx.y) * dim + c;
+        const long long step = 2ll * kSumWarps * dim;
+        // two CTAs' rows per SM in one trip to L2; the addresses are stepped, since a
+        // kernel this short waits for its own code (a product per load: 18.8 and
+        // 17.1 instead of 16.2 us for the whole backward pass of 4099 x 1025 and
+        // 16384 x 768; eight loads at a time with a remainder loop 17.1 and 17.3)
+        constexpr int kAhead = 10;
+#pragma unroll 1
+        for (int left = nparts - warp; left > 0; left -= kAhead * kSumWarps) {
+            float v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                v[k] = left > k * kSumWarps ? *p : 0.f;
+                p += step;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) s += v[k];
+        }
     }
     red[warp][lane] = s;
     __syncthreads();
