@@ -25,14 +25,14 @@
 // written in the first launch, before the sums: loads beside a memory system
 // that takes writes at its full rate are several times slower (zeroing CTAs
 // among the summing ones: 35-39 instead of 31 us for 8192 tokens of 50257 x
-// 768, 236-400 instead of 217 us for 16384 of 128256 x 4096).
+// 768, 236-400 instead of 216 us for 16384 of 128256 x 4096).
 //
 // Sums are fp32 and rounded once to the gradient's type.
 //
 // Measured (bf16): lookup of 16384 tokens from 128256 x 4096 35 us, 134 MB
 // written and up to as much read (the repeats come from L2); 16 tokens 1.9 us
 // on the GPU.  Gradient of 8192 tokens of 50257 x 768 30.8 us (13.9 us at the
-// copy rate), of 16384 of 128256 x 4096 217 us (183), of 1237 of 5003 x 333
+// copy rate), of 16384 of 128256 x 4096 215 us (183), of 1237 of 5003 x 333
 // fp32 15.3 us.
 #include <algorithm>
 

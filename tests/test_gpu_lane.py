@@ -460,3 +460,20 @@ def test_head_loss_of_confident_rows():
     ref.close(loss, vloss, x * (torch.expm1(2 * el) + 2.0 ** -19) + additions * ref.U + 4 * ref.U * vloss)
     assert (loss >= 0).all()
     assert loss[-1] < 1e-6
+
+
+@pytest.mark.parametrize("n,vocab,dim", [(1, 300, 64), (61, 20000, 72), (255, 20000, 256), (256, 40000, 64), (257, 20000, 64)])
+@pytest.mark.parametrize("index", [torch.int32, torch.int64])
+def test_head_loss_one_row_block(n, vocab, dim, index):
+    # batches of one block of 256 rows: more vocabulary tiles than CTA pairs, ignored rows of NaN and infinities
+    h, w, t, dloss = head_case(n, vocab, dim, 98 + n, 0.4)
+    off = t == -100
+    h[off] = float("nan")
+    h[off & (torch.arange(n, device=DEV) % 2 == 0)] = float("inf")
+    t = t.to(index)
+    loss, lse, dh, _ = check_head(h, w, t, dloss)
+    assert (loss[off] == 0).all() and (lse[off] == 0).all() and (dh[off] == 0).all()
+    t[:] = -100
+    loss, lse = mo.muon_head_loss(h, w, t)
+    assert (loss == 0).all() and (lse == 0).all()
+    status_ok()
