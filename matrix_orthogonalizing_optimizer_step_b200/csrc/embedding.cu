@@ -385,12 +385,21 @@ __device__ __forceinline__ unsigned digit_peers(unsigned d, int bits, bool on) {
 // consecutive pairs; a pair's place is the count of its digit in earlier CTAs,
 // tiles, warps, rows and lanes.  A stretch of one tile (any count up to
 // kCluster * kSortTile) is read once per pass.
+//
+// The caller has arrived at the cluster's barrier: the wait for the other CTAs'
+// arrival, which says that they run and their shared memory may be written,
+// stands before the first digit counts are sent.
 __device__ void sort_cluster(const SortArgs& S, SortShared& sh, int rank) {
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int bins = 1 << S.digit_bits;
     const unsigned len = ((S.count + kCluster - 1) / kCluster + 31) / 32 * 32;
     const unsigned lo = min(static_cast<unsigned>(rank) * len, S.count), hi = min(lo + len, S.count);
     const bool one_tile = len <= kSortTile;
+    bool peers_run = false;
+    auto await_peers = [&] {
+        if (!peers_run) cluster_wait();
+        peers_run = true;
+    };
     for (int p = 0; p < S.passes; ++p) {
         const unsigned* kin = S.keys[p & 1];
         const unsigned* pin = S.pos[p & 1];
@@ -406,6 +415,7 @@ __device__ void sort_cluster(const SortArgs& S, SortShared& sh, int rank) {
                 atomicAdd(&sh.base[(key_of(i) >> shift) & (bins - 1)], 1u);
             __syncthreads();
             const unsigned mine = tid < bins ? sh.base[tid] : 0;
+            await_peers();
             sort_bases(sh, bins, rank, mine);
         }
         // (a stretch without pairs still takes part in the exchange)
@@ -449,10 +459,12 @@ __device__ void sort_cluster(const SortArgs& S, SortShared& sh, int rank) {
                     tile += n[w];
                 }
             }
-            if (one_tile)
+            if (one_tile) {
+                await_peers();
                 sort_bases(sh, bins, rank, tile);
-            else
+            } else {
                 __syncthreads();
+            }
 #pragma unroll
             for (int r = 0; r < kItems; ++r) {
                 if (!on[r]) continue;
@@ -486,9 +498,11 @@ __device__ void fill_zero(const FillArgs& F, int cta, int ctas) {
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
     sort_and_fill_kernel(const SortArgs S, const FillArgs F) {
     extern __shared__ uint4 sort_smem[];
+    const bool sorts = blockIdx.x < kCluster;  // the first cluster
+    if (sorts && S.passes > 0) cluster_arrive();
     const long long i0 = static_cast<long long>(blockIdx.x) * kSortThreads + threadIdx.x;
     for (long long i = i0; i < S.ndone; i += static_cast<long long>(gridDim.x) * kSortThreads) S.done[i] = 0;
-    if (blockIdx.x < kCluster) {
+    if (sorts) {
         sort_cluster(S, *reinterpret_cast<SortShared*>(sort_smem), static_cast<int>(blockIdx.x));
         return;
     }
