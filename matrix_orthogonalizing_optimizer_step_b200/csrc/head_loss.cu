@@ -720,6 +720,15 @@ __device__ __forceinline__ bool counts(const RowsArgs& A, long long y) {
     return y != A.ignore && y >= 0 && y < A.vocab;
 }
 
+// End of CTA `cta`'s stretch of `per` tokens; cta * per + per may pass 2^31 where
+// the tokens do not.
+__host__ __device__ constexpr int rows_end(unsigned cta, int per, int tokens) {
+    const unsigned end = cta * static_cast<unsigned>(per) + static_cast<unsigned>(per);
+    return end < static_cast<unsigned>(tokens) ? static_cast<int>(end) : tokens;
+}
+static_assert(rows_end(0, 32, 20) == 20 && rows_end(1, 32, 100) == 64, "stretches");
+static_assert(rows_end(255, 1 << 23, 0x7fffffff - 1024) == 0x7fffffff - 1024, "the most tokens a call may have");
+
 // Finds the place of every row that counts among those that do and, if some do
 // not, copies the ones that do together, in order; the copied rows up to the
 // next multiple of 256 are zeroed.  A CTA has `per` tokens and counts all
@@ -732,7 +741,7 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs 
     __shared__ int dst_of[kRowsThreads];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     allow_successor();
-    const int t0 = blockIdx.x * per, t1 = min(t0 + per, A.tokens);
+    const int t0 = blockIdx.x * per, t1 = rows_end(blockIdx.x, per, A.tokens);
     int before = 0, all = 0;
     float top = 0.f;
 #pragma unroll 8
@@ -807,8 +816,8 @@ __global__ void __launch_bounds__(kRowsThreads) head_rows_kernel(const RowsArgs 
     }
     if (all == A.tokens) return;
     // rows behind the last
-    const int end = max(BMP, (all + BMP - 1) / BMP * BMP);
-    for (int r = all + blockIdx.x * kRowsWarps + warp; r < end; r += gridDim.x * kRowsWarps) {
+    const unsigned end = max(BMP, (all + BMP - 1) / BMP * BMP);
+    for (unsigned r = all + blockIdx.x * kRowsWarps + warp; r < end; r += gridDim.x * kRowsWarps) {
         uint4* dst = reinterpret_cast<uint4*>(A.rows + static_cast<long long>(r) * A.dim);
         for (int u = lane; u < units; u += 32) dst[u] = make_uint4(0, 0, 0, 0);
     }

@@ -41,3 +41,19 @@ def test_sorting_cluster_waits_for_its_peers_before_it_writes_to_them():
     for at in calls:
         assert re.search(r"await_peers\(\);\s*$", sort[:at])
     assert "cluster_wait()" in body(sort, r"auto await_peers = ")
+
+
+def test_rows_near_the_most_tokens_stay_in_range():
+    """The launch that finds the head's rows handles up to 2^31 - 1025 tokens in
+    at most 256 stretches of a multiple of 32, and zeroes rows from behind the
+    last that counts on: neither index may wrap.  (The sums of the signed form
+    pass 2^31, which this shows; the kernel's own form is asserted where it
+    stands.)"""
+    tokens = 2 ** 31 - 1025
+    per = -(-(-(-tokens // 256)) // 32) * 32
+    last = -(-tokens // per) - 1
+    assert last * per < tokens and last * per + per > 2 ** 31 - 1 >= tokens
+    assert tokens - 1 + last * 32 + 31 > 2 ** 31 - 1
+    kernel = body(source("head_loss.cu"), r"head_rows_kernel\(const")
+    assert "t1 = rows_end(blockIdx.x, per, A.tokens)" in kernel
+    assert re.search(r"for \(unsigned r = all \+ ", kernel)
