@@ -28,11 +28,15 @@
  *    (default: the legacy default stream).  No call synchronises the host
  *    except muon_device_status and muon_profile_read.
  *  - The library owns a cached device workspace sized for the last shape set
- *    (released by muon_release_workspace or at unload).  Calls are not
- *    thread-safe; use one thread per library instance.  Calls may switch
+ *    (released by muon_release_workspace or at unload).  Calls that use it
+ *    are not thread-safe: one at a time.  Calls may switch
  *    streams: a call's use of the workspace is ordered after the previous
  *    call's, on whichever stream that ran (an event wait, not a host sync).
  *    The caller's own tensors are not synchronised across streams.
+ *  - The stream binding and the last error belong to the calling thread; a
+ *    thread that has bound no stream uses the one bound last by any thread.
+ *    The lane's layers (below) keep no state between calls: several threads
+ *    may call them at once, and beside a call that uses the workspace.
  *  - CUDA graphs: muon_step, muon_orthogonalize, muon_adamw_step and
  *    muon_hybrid_step may be captured (stream capture of the bound stream)
  *    once the same call has run before the capture: a capture never builds
@@ -143,7 +147,8 @@ MUON_API int muon_set_config(const muon_config* cfg);
 /* Copy the installed config into *cfg. */
 MUON_API int muon_get_config(muon_config* cfg);
 
-/* Bind the cudaStream_t (passed as void*) that all later work is enqueued on. NULL = default stream. */
+/* Bind the cudaStream_t (passed as void*) that all later work of this thread is enqueued on (and that of
+ * threads that bind none). NULL = default stream. */
 MUON_API int muon_set_stream(void* stream);
 
 /* Human-readable description of the last error of this thread ("" if none). */

@@ -95,9 +95,9 @@ const void* ptr(const Tensor& t) { return t.defined() ? t.const_data_ptr() : nul
 const void* ptr(const optional<Tensor>& t) { return t ? ptr(*t) : nullptr; }
 void* out_ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 
-// The tensors' device current and its current stream bound, for one call.  The
-// interpreter lock is held throughout, so a backward pass on another thread
-// cannot bind its stream in between.
+// The tensors' device current and its current stream bound, for one call.  A
+// binding belongs to its thread: backward passes run on autograd's threads,
+// beside whatever the program's own thread has enqueued or is enqueueing.
 struct Call {
     c10::cuda::CUDAGuard guard;
     explicit Call(const Tensor& t) : guard(t.device()) {

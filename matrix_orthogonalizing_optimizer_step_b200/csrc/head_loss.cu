@@ -58,6 +58,7 @@
 // Every wait is bounded; on expiry the kernel records a timeout in the device
 // status word, drains its copies and MMAs, frees tensor memory and exits.
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include <cuda.h>
@@ -950,8 +951,8 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 EncodeTiledFn encoder() {
-    static EncodeTiledFn fn = nullptr;
-    if (fn) return fn;
+    static std::atomic<EncodeTiledFn> fn{nullptr};
+    if (EncodeTiledFn known = fn.load()) return known;
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
@@ -959,7 +960,8 @@ EncodeTiledFn encoder() {
         cudaGetLastError();
         return nullptr;
     }
-    return fn = reinterpret_cast<EncodeTiledFn>(p);
+    fn = reinterpret_cast<EncodeTiledFn>(p);
+    return reinterpret_cast<EncodeTiledFn>(p);
 }
 
 enum Box { BOX_K = 0 /* 64 x 128 rows */, BOX_MN = 1 /* 64 x 64 rows */, BOX_STORE = 2 /* 64 bytes x 32 rows */ };
@@ -983,8 +985,8 @@ bool encode(CUtensorMap* m, Box box, const void* base, bool f32, long long cols,
 // The CTA pairs that can be resident at once: the grid of a persistent launch.
 template <int MODE>
 int max_pairs() {
-    static int cached = -1;
-    if (cached > 0) return cached;
+    static std::atomic<int> cached{-1};
+    if (const int known = cached.load(); known > 0) return known;
     if (cudaFuncSetAttribute(head_gemm_kernel<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(SMEM_BYTES)) != cudaSuccess)
         return 0;
@@ -1001,13 +1003,14 @@ int max_pairs() {
     cfg.numAttrs = 1;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, head_gemm_kernel<MODE>, &cfg) != cudaSuccess) return 0;
-    return cached = n;
+    cached = n;
+    return n;
 }
 
 template <int MODE>
 cudaError_t launch_gemm(const HeadGemm& G, long long tiles, cudaStream_t stream) {
     // the attribute belongs to the device: set once on each
-    static bool raised[64] = {};
+    static std::atomic<bool> raised[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

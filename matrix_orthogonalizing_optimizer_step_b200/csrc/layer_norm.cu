@@ -26,6 +26,8 @@
 // 11.7 us at the copy rate: rows' chains of latencies and the second launch),
 // 4099 x 1025 fp32 18.5 us (50 MB, 7.8 us: 4-byte copies, and a third of the
 // rows' 1536 places empty).
+#include <atomic>
+
 #include "lane.h"
 #include "pdl.h"
 #include "rows.cuh"
@@ -647,7 +649,7 @@ int backward_parts_bound(long long rows, int num_sms) {
 // CTAs of a persistent launch: what the row groups need, and no more than are
 // resident at once (asked once per instance: a property of the build).
 template <typename K>
-cudaError_t persistent_grid(K kernel, int threads, int smem, int num_sms, int& per_sm, long long need, int most_per_sm,
+cudaError_t persistent_grid(K kernel, int threads, int smem, int num_sms, std::atomic<int>& resident, long long need, int most_per_sm,
                             unsigned& grid) {
     // above the 48 KB that every kernel may use (static shared memory counts
     // too) the limit is raised, for the current device, on every call
@@ -655,11 +657,13 @@ cudaError_t persistent_grid(K kernel, int threads, int smem, int num_sms, int& p
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
+    int per_sm = resident.load(std::memory_order_relaxed);
     if (per_sm == 0) {
         int n = 0;
         const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
         if (e != cudaSuccess) return e;
         per_sm = n < 1 ? 1 : n;
+        resident.store(per_sm, std::memory_order_relaxed);
     }
     const long long most = static_cast<long long>(num_sms) * (per_sm < most_per_sm ? per_sm : most_per_sm);
     grid = static_cast<unsigned>(need < most ? need : most);
@@ -668,7 +672,7 @@ cudaError_t persistent_grid(K kernel, int threads, int smem, int num_sms, int& p
 
 template <typename T, class S>
 cudaError_t launch_norm(const NormFwd& L, int num_sms, cudaStream_t stream) {
-    static int per_sm = 0;
+    static std::atomic<int> per_sm{0};
     unsigned grid = 0;
     const long long need = (L.rows + RowCta<S::W>::rows - 1) / RowCta<S::W>::rows;
     const cudaError_t e = persistent_grid(norm_kernel<T, S>, S::threads, S::smem, num_sms, per_sm, need, 32, grid);
@@ -679,7 +683,7 @@ cudaError_t launch_norm(const NormFwd& L, int num_sms, cudaStream_t stream) {
 
 template <typename T, class S>
 cudaError_t launch_norm_grad(const NormBwd& L, int num_sms, cudaStream_t stream, float* part, int& parts) {
-    static int per_sm = 0;
+    static std::atomic<int> per_sm{0};
     unsigned grid = 0;
     const long long need = (L.rows + RowCta<S::W>::rows - 1) / RowCta<S::W>::rows;
     const cudaError_t e =

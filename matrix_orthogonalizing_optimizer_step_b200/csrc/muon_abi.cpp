@@ -12,6 +12,7 @@
 #include <cstring>
 #include <deque>
 #include <memory>
+#include <mutex>
 #include <string>
 #include <vector>
 
@@ -26,7 +27,12 @@ namespace {
 thread_local std::string g_err;
 muon_config g_cfg;
 bool g_cfg_init = false;
-cudaStream_t g_stream = nullptr;
+// A binding belongs to the thread that made it, so that autograd's threads,
+// which call the lane's layers, cannot move another thread's call to their
+// stream.  A thread that has bound none uses the last one bound by any.
+std::atomic<cudaStream_t> g_last_stream{nullptr};
+thread_local cudaStream_t t_stream = nullptr;
+thread_local bool t_bound = false;
 std::atomic<long long> g_launches{0};
 
 struct DeviceState {
@@ -54,6 +60,7 @@ struct DeviceState {
     std::vector<cudaEvent_t> ev_in, ev_done;  // per group: gradients landed, group stepped
 };
 std::deque<DeviceState> g_devs;  // deque: references stay valid on growth
+std::mutex g_devs_mutex;         // the list itself; a device's state belongs to one call at a time
 
 // Per-shape Newton-Schulz schedules of muon_step, keyed by the short and the
 // long side of the matrix.
@@ -116,7 +123,7 @@ int check_cfg(const muon_config& c) {
 // True while the bound stream is being captured into a CUDA graph.
 bool capturing() {
     cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(g_stream, &st) != cudaSuccess) {
+    if (cudaStreamIsCapturing(bound_stream(), &st) != cudaSuccess) {
         cudaGetLastError();
         return false;
     }
@@ -131,6 +138,7 @@ int device_state(DeviceState** out) {
         cudaGetLastError();
         return fail(MUON_ERR_CUDA, std::string("no CUDA device: ") + cudaGetErrorString(e));
     }
+    std::lock_guard<std::mutex> lock(g_devs_mutex);
     for (DeviceState& d : g_devs)
         if (d.device == dev) {
             *out = &d;
@@ -236,8 +244,8 @@ Profiler g_prof;
 // an earlier, uncaptured call is waited on.
 int ws_acquire(DeviceState* ds) {
     if (capturing()) return MUON_OK;
-    if (ds->ws_used && ds->ws_stream != g_stream) {
-        const cudaError_t e = cudaStreamWaitEvent(g_stream, ds->ws_event, 0);
+    if (ds->ws_used && ds->ws_stream != bound_stream()) {
+        const cudaError_t e = cudaStreamWaitEvent(bound_stream(), ds->ws_event, 0);
         if (e != cudaSuccess) return fail(MUON_ERR_CUDA, std::string("stream wait failed: ") + cudaGetErrorString(e));
     }
     return MUON_OK;
@@ -247,9 +255,9 @@ int ws_acquire(DeviceState* ds) {
 // under stream capture: the captured launches run when the graph does).
 int ws_release(DeviceState* ds) {
     if (capturing()) return MUON_OK;
-    const cudaError_t e = cudaEventRecord(ds->ws_event, g_stream);
+    const cudaError_t e = cudaEventRecord(ds->ws_event, bound_stream());
     if (e != cudaSuccess) return fail(MUON_ERR_CUDA, std::string("event record failed: ") + cudaGetErrorString(e));
-    ds->ws_stream = g_stream;
+    ds->ws_stream = bound_stream();
     ds->ws_used = true;
     return MUON_OK;
 }
@@ -276,9 +284,9 @@ int run_plan(DeviceState* ds, Plan& plan, const PlanRequest& rq, const AdamArgs*
     if (wst != MUON_OK) return wst;
     if (!plan.same_shape_key(rq)) {
         // tables of the previous plan may still be read by queued kernels
-        cudaError_t e = cudaStreamSynchronize(g_stream);
+        cudaError_t e = cudaStreamSynchronize(bound_stream());
         if (e != cudaSuccess) return fail(MUON_ERR_CUDA, std::string("stream sync failed: ") + cudaGetErrorString(e));
-        const int st = plan.build(rq, ds->status, ds->num_sms, g_stream, err);
+        const int st = plan.build(rq, ds->status, ds->num_sms, bound_stream(), err);
         if (st != MUON_OK) {
             plan.release();
             return fail(st, err);
@@ -288,7 +296,7 @@ int run_plan(DeviceState* ds, Plan& plan, const PlanRequest& rq, const AdamArgs*
     plan.set_index_base(rq.index_base);
     plan.set_adamw(adam ? &adam->L : nullptr, adam ? adam->bytes : 0.0);
     long long launched = 0;
-    const int st = plan.run(g_stream, g_prof.on ? &g_prof : nullptr, &launched, err);
+    const int st = plan.run(bound_stream(), g_prof.on ? &g_prof : nullptr, &launched, err);
     g_launches += launched;
     wst = ws_release(ds);
     if (st != MUON_OK) return fail(st, err);
@@ -415,7 +423,7 @@ int adamw_upload(DeviceState* ds, AdamArgs& aa) {
                     "stream capture needs the AdamW table in place: make the same call once before capturing it");
     if (ds->adam_cap < bytes) {
         if (ds->adam_table) {
-            cudaStreamSynchronize(g_stream);
+            cudaStreamSynchronize(bound_stream());
             cudaFree(ds->adam_table);
         }
         ds->adam_table = nullptr;
@@ -431,7 +439,7 @@ int adamw_upload(DeviceState* ds, AdamArgs& aa) {
         last.clear();
     }
     if (!same) {
-        cudaError_t e = cudaMemcpyAsync(ds->adam_table, t.data(), bytes, cudaMemcpyHostToDevice, g_stream);
+        cudaError_t e = cudaMemcpyAsync(ds->adam_table, t.data(), bytes, cudaMemcpyHostToDevice, bound_stream());
         if (e != cudaSuccess) return fail(MUON_ERR_CUDA, std::string("table upload failed: ") + cudaGetErrorString(e));
         last = t;
     }
@@ -510,7 +518,7 @@ int offload_resources(DeviceState* ds, int groups) {
 }  // namespace
 
 namespace muon {
-cudaStream_t bound_stream() { return g_stream; }
+cudaStream_t bound_stream() { return t_bound ? t_stream : g_last_stream.load(); }
 void set_last_error(const char* msg) { g_err = msg; }
 
 int abi_fail(int code, const char* msg) { return fail(code, msg); }
@@ -553,16 +561,19 @@ int muon_get_config(muon_config* cfg) {
 }
 
 int muon_set_stream(void* stream) {
-    g_stream = static_cast<cudaStream_t>(stream);
+    t_stream = static_cast<cudaStream_t>(stream);
+    t_bound = true;
+    g_last_stream = t_stream;
     return MUON_OK;
 }
 
 const char* muon_last_error(void) { return g_err.c_str(); }
 
 int muon_release_workspace(void) {
-    cudaStreamSynchronize(g_stream);
+    cudaStreamSynchronize(bound_stream());
     int cur = -1;
     cudaGetDevice(&cur);
+    std::lock_guard<std::mutex> lock(g_devs_mutex);
     for (DeviceState& d : g_devs) {
         if (d.ws_used) {
             cudaSetDevice(d.device);
@@ -588,7 +599,7 @@ int muon_device_status(int* bad_index) {
     DeviceState* ds = nullptr;
     int st = device_state(&ds);
     if (st != MUON_OK) return st;
-    cudaError_t e = cudaStreamSynchronize(g_stream);
+    cudaError_t e = cudaStreamSynchronize(bound_stream());
     if (e != cudaSuccess) return fail(MUON_ERR_CUDA, std::string("stream sync failed: ") + cudaGetErrorString(e));
     DeviceStatus h;
     e = cudaMemcpy(&h, ds->status, sizeof(h), cudaMemcpyDeviceToHost);
@@ -690,7 +701,7 @@ int muon_debug_corrupt_guard(int index) {
     if (index >= ds->plan->guard_count())
         return fail(MUON_ERR_INVALID_ARG, "no such guard (MUON_DEBUG_CANARY=1 and a plan built by muon_step or "
                                           "muon_orthogonalize are needed)");
-    const cudaError_t e = cudaMemsetAsync(ds->plan->guard_addr(index), 0, 1, g_stream);
+    const cudaError_t e = cudaMemsetAsync(ds->plan->guard_addr(index), 0, 1, bound_stream());
     if (e != cudaSuccess) return fail(MUON_ERR_CUDA, std::string("memset failed: ") + cudaGetErrorString(e));
     return MUON_OK;
 }
@@ -743,7 +754,7 @@ int muon_step_offload(void* const* params, const void* const* grads_host, void* 
         return fail(MUON_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
     };
     // the copies start after the work already queued on the bound stream
-    cudaError_t e = cudaEventRecord(ds->ev_start, g_stream);
+    cudaError_t e = cudaEventRecord(ds->ev_start, bound_stream());
     if (e == cudaSuccess) e = cudaStreamWaitEvent(ds->copy_in, ds->ev_start, 0);
     if (e == cudaSuccess) e = cudaStreamWaitEvent(ds->copy_out, ds->ev_start, 0);
     if (e != cudaSuccess) return cuda_fail(e, "stream ordering failed");
@@ -759,7 +770,7 @@ int muon_step_offload(void* const* params, const void* const* grads_host, void* 
     int k = 0;
     for (; k < ngroups && e == cudaSuccess; ++k) {
         if (grads_host) {
-            e = cudaStreamWaitEvent(g_stream, ds->ev_in[k], 0);
+            e = cudaStreamWaitEvent(bound_stream(), ds->ev_in[k], 0);
             if (e != cudaSuccess) break;
         }
         rqs[k].device = ds->device;
@@ -770,7 +781,7 @@ int muon_step_offload(void* const* params, const void* const* grads_host, void* 
         nvtxRangePop();
         if (st != MUON_OK) break;
         if (params_host) {
-            e = cudaEventRecord(ds->ev_done[k], g_stream);
+            e = cudaEventRecord(ds->ev_done[k], bound_stream());
             if (e == cudaSuccess) e = cudaStreamWaitEvent(ds->copy_out, ds->ev_done[k], 0);
             for (int i = bounds[k]; i < bounds[k + 1] && e == cudaSuccess; ++i)
                 e = cudaMemcpyAsync(params_host[i], params[i], elems(i) * psz, cudaMemcpyDeviceToHost, ds->copy_out);
@@ -779,9 +790,9 @@ int muon_step_offload(void* const* params, const void* const* grads_host, void* 
     const std::string run_err = st != MUON_OK ? g_err : std::string();
     // join: work queued on the bound stream after this call follows every copy
     cudaError_t j = cudaEventRecord(ds->ev_out, ds->copy_out);
-    if (j == cudaSuccess) j = cudaStreamWaitEvent(g_stream, ds->ev_out, 0);
+    if (j == cudaSuccess) j = cudaStreamWaitEvent(bound_stream(), ds->ev_out, 0);
     if (j == cudaSuccess && grads_host) j = cudaEventRecord(ds->ev_out, ds->copy_in);
-    if (j == cudaSuccess && grads_host) j = cudaStreamWaitEvent(g_stream, ds->ev_out, 0);
+    if (j == cudaSuccess && grads_host) j = cudaStreamWaitEvent(bound_stream(), ds->ev_out, 0);
     if (st != MUON_OK) return fail(st, run_err);
     if (e != cudaSuccess) return cuda_fail(e, "offload copy or ordering failed");
     if (j != cudaSuccess) return cuda_fail(j, "stream join failed");
@@ -845,13 +856,13 @@ int muon_adamw_step(void* const* params, const void* const* grads, void* const* 
     if (st != MUON_OK) return st;
     st = adamw_upload(ds, aa);
     if (st != MUON_OK) return st;
-    if (g_prof.on) g_prof.before(g_stream);
+    if (g_prof.on) g_prof.before(bound_stream());
     nvtxRangePushA("muon adamw");
-    cudaError_t e = launch_adamw(aa.L, g_stream);
+    cudaError_t e = launch_adamw(aa.L, bound_stream());
     nvtxRangePop();
     if (e != cudaSuccess) return fail(MUON_ERR_CUDA, std::string("kernel launch failed: ") + cudaGetErrorString(e));
     ++g_launches;
-    if (g_prof.on) g_prof.after(g_stream, 4, 0.0, aa.bytes);
+    if (g_prof.on) g_prof.after(bound_stream(), 4, 0.0, aa.bytes);
     return ws_release(ds);
 }
 
