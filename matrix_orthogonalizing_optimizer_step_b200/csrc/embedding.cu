@@ -528,18 +528,31 @@ constexpr int kRunWarps = 4;
 
 // Chunks behind `chunk` (up) or before it (down) that the run of `key` reaches
 // into: up, the later chunks that start with it, down, the earlier ones that
-// end with it (whole warp; 32 chunks per look).
+// end with it (whole warp).  Equal keys lie together, so a chunk that the run
+// does not reach ends it: one look at the 32 nearest chunks, then at doubling
+// distances, then at 32 places between the last hit and the first miss until
+// they meet.  A run of m chunks costs each of them log m looks (2^21 equal
+// tokens, 8 wide: 6.7 ms, almost all of it the joining warp's; with looks at 32
+// chunks at a time to the run's end 56 ms).
 __device__ __forceinline__ unsigned chunks_of_run(const RunArgs& R, unsigned chunk, unsigned key, bool up, int lane) {
-    unsigned m = 0;
-    while (true) {
-        const unsigned k = m + 1 + lane;  // so many chunks away
-        const unsigned long long at = up ? (static_cast<unsigned long long>(chunk) + k) * kChunk
-                                         : (static_cast<unsigned long long>(chunk) + 1 - k) * kChunk - 1;
+    auto misses = [&](unsigned long long k) {  // lanes whose chunk, k away, the run does not reach
+        const unsigned long long at = up ? (chunk + k) * kChunk : (chunk + 1ull - k) * kChunk - 1;
         const bool in = up ? at < R.count : k <= chunk;
-        const unsigned miss = __ballot_sync(0xffffffffu, !(in && R.keys[in ? at : 0] == key));
-        if (miss) return m + __ffs(miss) - 1;
-        m += 32;
+        return __ballot_sync(0xffffffffu, !(in && R.keys[in ? at : 0] == key));
+    };
+    unsigned miss = misses(lane + 1);
+    if (miss) return __ffs(miss) - 1;
+    miss = misses(64ull << lane);  // (behind the last chunk from the 27th lane on at the latest)
+    const int first = __ffs(miss) - 1;
+    unsigned long long hit = 32ull << first, end = 64ull << first;  // the run reaches `hit` chunks, not `end`
+    while (end - hit > 1) {
+        const unsigned long long step = (end - hit + 31) / 32;
+        const unsigned long long k = min(hit + step * (lane + 1), end);
+        const int f = __ffs(misses(k)) - 1;  // the last lane's is `end`
+        end = min(hit + step * (f + 1), end);
+        hit += step * f;
     }
+    return static_cast<unsigned>(hit);
 }
 
 // A warp adds the rows of one chunk for 256 columns: items of equal size with

@@ -1,0 +1,71 @@
+"""The AdamW lane's layers at inputs where a kernel can be right and slow, or
+right nearly everywhere: long runs and crowded classes of tokens, rows of huge
+values, targets' entries of the head's gradients, frozen parameters."""
+import math
+
+import pytest
+import torch
+
+import matrix_orthogonalizing_optimizer_step_b200 as mo
+from matrix_orthogonalizing_optimizer_step_b200 import layers
+from tests import _lane_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def status_ok():
+    assert mo.muon_device_status(DEV) == (mo.MUON_OK, -1)
+
+
+def best_us(f, repeats=5):
+    """Shortest of `repeats` timings of one call, after two calls."""
+    f(), f()
+    best = math.inf
+    for _ in range(repeats):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        torch.cuda.synchronize()
+        a.record()
+        f()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+def integer_sums(t, g, vocab):
+    """The table's gradient of integers: every order of additions gives it (sums below 2^24)."""
+    return torch.zeros(vocab, g.shape[1], device=DEV, dtype=torch.float64).index_add_(0, t, g.double())
+
+
+# ---- embedding gradient --------------------------------------------------------------
+
+
+@pytest.mark.parametrize("n", [300_000, 700_001])
+def test_embedding_backward_long_runs(n):
+    """Runs of several hundred thousand equal tokens: from the first position,
+    to the last, between others, and two that meet inside a chunk."""
+    vocab, dim = 50, 24
+    g = torch.randint(-3, 4, (n, dim), generator=gen(1), device=DEV).float()
+    i = torch.arange(n, device=DEV)
+    for t in (torch.full((n,), 7, device=DEV), torch.where(i < 5, 3, 7), torch.where(i < 77, 49, 7),
+              torch.where(i % 2 == 0, 11, 12), torch.where(i % 1000 == 0, 1 + i // 1000 % 49, 20)):
+        got = mo.muon_embedding_backward(t, g, vocab)
+        assert torch.equal(got.double(), integer_sums(t, g, vocab))
+    status_ok()
+
+
+def test_embedding_backward_time_grows_with_the_run():
+    """Four times the tokens in one run take about four times as long.  (A walk
+    along the run from each of its chunks takes sixteen times as many steps.)"""
+    times = []
+    for n in (1 << 19, 1 << 21):
+        g = torch.ones(n, 8, device=DEV)
+        t = torch.zeros(n, dtype=torch.int64, device=DEV)
+        times.append(best_us(lambda: mo.muon_embedding_backward(t, g, 4)))
+    assert times[1] < 8 * times[0], times
