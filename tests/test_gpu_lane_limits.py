@@ -69,3 +69,15 @@ def test_embedding_backward_time_grows_with_the_run():
         t = torch.zeros(n, dtype=torch.int64, device=DEV)
         times.append(best_us(lambda: mo.muon_embedding_backward(t, g, 4)))
     assert times[1] < 8 * times[0], times
+
+
+def test_embedding_backward_time_of_one_class():
+    """Tokens that one CTA of the first launch owns take that CTA a pass over
+    them, not a pass per row: a few times the time of tokens spread over all CTAs."""
+    sms = torch.cuda.get_device_properties(DEV).multi_processor_count
+    n, vocab = 16384, 2000 * sms
+    g = torch.ones(n, 8, device=DEV)
+    i = torch.arange(n, device=DEV)
+    spread = best_us(lambda t=i * 17 % vocab: mo.muon_embedding_backward(t, g, vocab))
+    crowded = best_us(lambda t=i % 2000 * sms: mo.muon_embedding_backward(t, g, vocab))
+    assert crowded < 8 * spread, (spread, crowded)
