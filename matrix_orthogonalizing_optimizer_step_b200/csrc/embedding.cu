@@ -10,22 +10,23 @@
 // The gradient puts the tokens in order, so that each table row is summed by
 // whoever owns its stretch of the order and no atomic add is needed: every sum
 // is in the order of the tokens' positions and results repeat bit for bit.
-//   1. one launch orders (token, position) pairs and writes zeros over the
-//      table.  Up to 16384 tokens: one CTA per SM owns a class of the
-//      vocabulary, finds its tokens among all and groups them, then zeroes the
-//      rows that none asks for.  More tokens: a cluster of 8 CTAs sorts them
-//      while all other CTAs zero the table.
-//   2. the order is cut into chunks of 16 positions; a warp sums the rows of
+//   1. one launch orders (token, position) pairs.  Up to 16384 tokens: one CTA
+//      per SM owns a class of the vocabulary, finds its tokens among all and
+//      groups them.  More tokens: a cluster of 8 CTAs sorts them.
+//   2. zeros are written over the table, beside the first launch, by one of
+//      their own; where a large part of the rows is asked for, or the table is
+//      small, by the classes' CTAs after their grouping, over the other rows.
+//   3. the order is cut into chunks of 16 positions; a warp sums the rows of
 //      one chunk for 256 columns.  A token whose run lies inside a chunk is
 //      written at once.  A run that crosses chunk borders leaves one fp32
 //      partial row per chunk, and the warp that finishes the last of the run's
 //      chunks adds them in order.
 // The cut at fixed positions keeps a frequent token (or a padding token that
 // fills half a batch) from becoming one warp's serial loop.  The zeros are
-// written in the first launch, before the sums: loads beside a memory system
-// that takes writes at its full rate are several times slower (zeroing CTAs
-// among the summing ones: 35-39 instead of 31 us for 8192 tokens of 50257 x
-// 768, 236-400 instead of 216 us for 16384 of 128256 x 4096).
+// written before the sums: loads beside a memory system that takes writes at
+// its full rate are several times slower (zeroing CTAs among the summing ones:
+// 35-39 instead of 31 us for 8192 tokens of 50257 x 768, 236-400 instead of 216 us
+// for 16384 of 128256 x 4096).
 //
 // Sums are fp32 and rounded once to the gradient's type.
 //
@@ -124,6 +125,7 @@ struct ClassArgs {
     unsigned* pos;      // their positions
     unsigned* done;     // counters to zero for the adding launch
     int ndone;
+    int zero;           // write zeros over the rows that no token asks for
     void* out;
     long long dim;
     DeviceStatus* status;
@@ -149,8 +151,8 @@ __device__ __forceinline__ void zero_row(TO* row, long long dim, int lane) {
 
 // CTA c owns the table rows c, c + classes, c + 2 classes, ...: it finds the
 // tokens of its class among all (each CTA reads all of them, from L2) and
-// groups them by row in the order of their positions.  Then it writes zeros
-// over the rows that no token asks for.  The order is ready after 4 us (8192
+// groups them by row in the order of their positions.  Then, where no launch of
+// its own does it, it writes zeros over the rows that no token asks for.  The order is ready after 4 us (8192
 // tokens), where the sort's two passes take 20: no step of it leaves the CTA.
 template <typename TO>
 __global__ void __launch_bounds__(kClassThreads) class_group_kernel(const ClassArgs A) {
@@ -276,11 +278,12 @@ __global__ void __launch_bounds__(kClassThreads) class_group_kernel(const ClassA
     }
     if (cls == classes - 1)  // tokens that take no part
         for (int k = before + total + tid; k < A.count; k += kClassThreads) A.keys[k] = A.vocab;
+    if (!A.zero) return;
     for (int r = warp; r < rows; r += kClassWarps)
         if (count[r] == 0) zero_row(static_cast<TO*>(A.out) + static_cast<long long>(cls + r * classes) * A.dim, A.dim, lane);
 }
 
-// ---- gradient: sort and zero fill -----------------------------------------------
+// ---- gradient: order by sorting, zeros -----------------------------------------------
 
 constexpr int kCluster = 8;
 constexpr int kSortThreads = 1024;
@@ -302,11 +305,6 @@ struct SortArgs {
     unsigned* done;          // counters to zero for the adding launch
     long long ndone;
     DeviceStatus* status;
-};
-
-struct FillArgs {
-    void* out;
-    long long bytes;
 };
 
 struct SortShared {
@@ -484,33 +482,37 @@ __device__ void sort_cluster(const SortArgs& S, SortShared& sh, int rank) {
     }
 }
 
-// Zeros over the table (the runs' rows are written by the next launch), by
-// CTA `cta` of `ctas`: whole 16-byte units from the first aligned address on.
-__device__ void fill_zero(const FillArgs& F, int cta, int ctas) {
-    const long long nthr = static_cast<long long>(ctas) * kSortThreads;
-    const long long i0 = static_cast<long long>(cta) * kSortThreads + threadIdx.x;
-    char* base = static_cast<char*>(F.out);
-    const long long head = min(static_cast<long long>((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15), F.bytes);
-    const long long n16 = (F.bytes - head) / 16;
-    uint4* q = reinterpret_cast<uint4*>(base + head);
-    for (long long i = i0; i < n16; i += nthr) q[i] = make_uint4(0, 0, 0, 0);
-    const long long tail = head + n16 * 16;
-    if (i0 < head) base[i0] = 0;
-    if (i0 < F.bytes - tail) base[tail + i0] = 0;
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads) sort_kernel(const SortArgs S) {
+    extern __shared__ uint4 sort_smem[];
+    cluster_arrive();
+    allow_successor();
+    const long long i0 = static_cast<long long>(blockIdx.x) * kSortThreads + threadIdx.x;
+    for (long long i = i0; i < S.ndone; i += kCluster * kSortThreads) S.done[i] = 0;
+    sort_cluster(S, *reinterpret_cast<SortShared*>(sort_smem), static_cast<int>(blockIdx.x));
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
-    sort_and_fill_kernel(const SortArgs S, const FillArgs F) {
-    extern __shared__ uint4 sort_smem[];
-    const bool sorts = blockIdx.x < kCluster;  // the first cluster
-    if (sorts && S.passes > 0) cluster_arrive();
-    const long long i0 = static_cast<long long>(blockIdx.x) * kSortThreads + threadIdx.x;
-    for (long long i = i0; i < S.ndone; i += static_cast<long long>(gridDim.x) * kSortThreads) S.done[i] = 0;
-    if (sorts) {
-        sort_cluster(S, *reinterpret_cast<SortShared*>(sort_smem), static_cast<int>(blockIdx.x));
-        return;
-    }
-    fill_zero(F, static_cast<int>(blockIdx.x) - kCluster, static_cast<int>(gridDim.x) - kCluster);
+// Zeros over the whole table, beside the launch that orders the tokens, which
+// is its predecessor: whole 16-byte units from the first aligned address on.
+// Short CTAs in the order of the addresses write 7.5 TB/s, as much as a memset;
+// persistent ones, which drift apart, 6.3 in any pattern (2.1 GB: 280 and 330-340
+// us; 16-byte, 32-byte and bulk stores and cache hints alike).
+constexpr int kZeroThreads = 256;
+constexpr int kZeroUnits = 4;
+constexpr long long kZeroBytes = 16ll * kZeroThreads * kZeroUnits;  // of a CTA
+__global__ void __launch_bounds__(kZeroThreads) zero_kernel(char* base, long long bytes) {
+    allow_successor();
+    const long long head = min(static_cast<long long>((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15), bytes);
+    const long long n16 = (bytes - head) / 16;
+    uint4* q = reinterpret_cast<uint4*>(base + head);
+    const long long i0 = static_cast<long long>(blockIdx.x) * (kZeroThreads * kZeroUnits) + threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < kZeroUnits; ++u)
+        if (i0 + u * kZeroThreads < n16) q[i0 + u * kZeroThreads] = make_uint4(0, 0, 0, 0);
+    if (blockIdx.x > 0) return;
+    const long long tail = head + n16 * 16;
+    if (threadIdx.x < head) base[threadIdx.x] = 0;
+    if (threadIdx.x < bytes - tail) base[tail + threadIdx.x] = 0;
+    wait_predecessor();  // one CTA is enough for this launch to end after it
 }
 
 // ---- gradient: sums over runs of equal tokens ------------------------------------
@@ -738,8 +740,8 @@ BwdLayout bwd_layout(long long count, long long dim) {
     return l;
 }
 
-// Orders up to kClassTokens tokens into keys[0], pos[0] and fills the table with zeros.
-cudaError_t launch_class_group(const EmbedBwd& L, int classes, const BwdLayout& lay, cudaStream_t stream) {
+// Orders up to kClassTokens tokens into keys[0], pos[0]; `zero`: and fills the table with zeros.
+cudaError_t launch_class_group(const EmbedBwd& L, int classes, bool zero, const BwdLayout& lay, cudaStream_t stream) {
     char* ws = static_cast<char*>(L.workspace);
     ClassArgs A{};
     A.tokens = L.tokens;
@@ -753,6 +755,7 @@ cudaError_t launch_class_group(const EmbedBwd& L, int classes, const BwdLayout& 
     A.pos = reinterpret_cast<unsigned*>(ws + lay.pos[0]);
     A.done = reinterpret_cast<unsigned*>(ws + lay.done);
     A.ndone = static_cast<int>(lay.ndone);
+    A.zero = zero;
     A.out = L.out;
     A.dim = L.dim;
     A.status = L.status;
@@ -768,8 +771,8 @@ cudaError_t launch_class_group(const EmbedBwd& L, int classes, const BwdLayout& 
     return cudaGetLastError();
 }
 
-// The same for any number of tokens, by sorting; *side says which pair of buffers has the result.
-cudaError_t launch_sort(const EmbedBwd& L, int num_sms, const BwdLayout& lay, cudaStream_t stream, int* side) {
+// Orders any number of tokens by sorting; *side says which pair of buffers has the result.
+cudaError_t launch_sort(const EmbedBwd& L, const BwdLayout& lay, cudaStream_t stream, int* side) {
     char* ws = static_cast<char*>(L.workspace);
     SortArgs S{};
     S.tokens = L.tokens;
@@ -783,22 +786,26 @@ cudaError_t launch_sort(const EmbedBwd& L, int num_sms, const BwdLayout& lay, cu
     }
     int bits = 1;
     while ((static_cast<unsigned long long>(L.vocab + 1) >> bits) != 0) ++bits;  // keys are 0 .. vocab + 1
-    S.passes = L.count > 0 ? (bits + kMaxBits - 1) / kMaxBits : 0;
-    S.digit_bits = S.passes ? (bits + S.passes - 1) / S.passes : 0;
+    S.passes = (bits + kMaxBits - 1) / kMaxBits;
+    S.digit_bits = (bits + S.passes - 1) / S.passes;
     S.done = reinterpret_cast<unsigned*>(ws + lay.done);
     S.ndone = static_cast<long long>(lay.ndone);
     S.status = L.status;
     *side = S.passes & 1;
-    FillArgs F{L.out, L.vocab * L.dim * dtype_size(L.out_dt)};
-    // two CTAs of 1024 threads per SM; no more than the fill has 16-byte units for
-    long long fill = (F.bytes / 16 + kSortThreads - 1) / kSortThreads;
-    const long long most = static_cast<long long>(num_sms) * 2 / kCluster * kCluster - kCluster;
-    fill = fill < 1 ? 1 : (fill > most ? most : fill);
-    const unsigned grid = static_cast<unsigned>((fill + kCluster - 1) / kCluster * kCluster + kCluster);
-    const cudaError_t e = cudaFuncSetAttribute(sort_and_fill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(sizeof(SortShared)));
+    const cudaError_t e =
+        cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(sizeof(SortShared)));
     if (e != cudaSuccess) return e;
-    sort_and_fill_kernel<<<grid, kSortThreads, sizeof(SortShared), stream>>>(S, F);
+    sort_kernel<<<kCluster, kSortThreads, sizeof(SortShared), stream>>>(S);
+    return cudaGetLastError();
+}
+
+// Zeros over the table; after a launch of this call that orders the tokens, or on its own.
+cudaError_t launch_zero(const EmbedBwd& L, bool dependent, cudaStream_t stream) {
+    const long long bytes = L.vocab * L.dim * dtype_size(L.out_dt);
+    const unsigned blocks = static_cast<unsigned>((bytes + kZeroBytes - 1) / kZeroBytes);
+    char* out = static_cast<char*>(L.out);
+    if (dependent) return launch_dependent(zero_kernel, dim3(blocks), kZeroThreads, 0, stream, out, bytes);
+    zero_kernel<<<blocks, kZeroThreads, 0, stream>>>(out, bytes);
     return cudaGetLastError();
 }
 
@@ -840,9 +847,25 @@ cudaError_t launch_embedding_backward(const EmbedBwd& L, int num_sms, cudaStream
     const int classes = static_cast<int>(std::min<long long>(std::min(num_sms, kMostClasses), L.vocab));
     const bool by_class = L.count > 0 && L.count <= kClassTokens && L.vocab <= kClassVocab &&
                           (L.vocab + classes - 1) / classes <= kClassRows;
+    // The zeros' own launch writes 7.5 TB/s from the first microsecond on and the
+    // rows that tokens ask for twice, the classes' CTAs 6.3 TB/s of the others
+    // after 4-10 us of ordering: even where a sixth of the rows is asked for.  (8192
+    // tokens of 50257 x 768 bf16 22.8-26.6 instead of 24.1-28.6 us, 16384 of 128256 x
+    // 4096 190 instead of 203-212, 300 of 128256 x 2001 fp32 147 instead of 194.)  A
+    // launch more costs as much as it gains below 8 MiB (300 of 2500 x 768 fp32: 10.4
+    // and 10.3).
+    constexpr long long kZeroApart = 8ll << 20;
+    const bool zero_apart = !by_class || (L.vocab * L.dim * dtype_size(L.out_dt) >= kZeroApart && L.count * 6 <= L.vocab);
     int side = 0;
-    cudaError_t e = by_class ? launch_class_group(L, classes, lay, stream) : launch_sort(L, num_sms, lay, stream, &side);
-    ++*launches;
+    cudaError_t e = cudaSuccess;
+    if (L.count > 0) {
+        e = by_class ? launch_class_group(L, classes, !zero_apart, lay, stream) : launch_sort(L, lay, stream, &side);
+        ++*launches;
+    }
+    if (e == cudaSuccess && zero_apart) {
+        e = launch_zero(L, L.count > 0, stream);
+        ++*launches;
+    }
     if (e != cudaSuccess || L.count == 0) return e;
 
     RunArgs R{};

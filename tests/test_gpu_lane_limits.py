@@ -81,3 +81,31 @@ def test_embedding_backward_time_of_one_class():
     spread = best_us(lambda t=i * 17 % vocab: mo.muon_embedding_backward(t, g, vocab))
     crowded = best_us(lambda t=i % 2000 * sms: mo.muon_embedding_backward(t, g, vocab))
     assert crowded < 8 * spread, (spread, crowded)
+
+
+@pytest.mark.parametrize("vocab,dim", [(128256, 2001), (128256, 1000), (50257, 768)])
+def test_embedding_backward_of_few_tokens_is_a_zero_fill(vocab, dim):
+    """An fp32 table and 300 tokens: writing the zeros is all there is to do, and
+    that goes as fast as torch's zeros with an index_add_ (a tenth for the clock)."""
+    g = torch.randn(300, dim, generator=gen(5), device=DEV)
+    t = torch.randint(0, vocab, (300,), generator=gen(6), device=DEV)
+    plain = best_us(lambda: [torch.zeros(vocab, dim, device=DEV).index_add_(0, t, g) for _ in range(10)])
+    own = best_us(lambda: [mo.muon_embedding_backward(t, g, vocab) for _ in range(10)])
+    assert own < 1.1 * plain, (own / 10, plain / 10)
+
+
+@pytest.mark.parametrize("vocab,dim,offset", [(70_001, 40, 0), (70_001, 333, 1), (400_003, 9, 3)])
+@pytest.mark.parametrize("n", [0, 1, 300])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_embedding_backward_zeros_of_large_tables(vocab, dim, offset, n, dtype):
+    """Zeros beside the ordering: any alignment of the table, every element of it
+    and none around it, with tokens in the first and last row."""
+    flat = torch.full((vocab * dim + 16,), 5.0, device=DEV, dtype=dtype)
+    out = flat[offset:offset + vocab * dim].view(vocab, dim)
+    g = torch.randint(-3, 4, (n, dim), generator=gen(7), device=DEV).to(dtype)
+    t = torch.randint(0, vocab, (n,), generator=gen(8), device=DEV)
+    t[:1], t[n // 2:n // 2 + 1] = vocab - 1, 0
+    mo.muon_embedding_backward(t, g, vocab, out=out)
+    assert torch.equal(out.double(), integer_sums(t, g, vocab))
+    assert (flat[:offset] == 5).all() and (flat[offset + vocab * dim:] == 5).all()
+    status_ok()

@@ -33,7 +33,7 @@ def test_sorting_cluster_waits_for_its_peers_before_it_writes_to_them():
     wait directly before it."""
     text = source("embedding.cu")
     assert text.count("st.shared::cluster") == body(text, r"void sort_bases\(").count("st.shared::cluster") == 1
-    kernel = body(text, r"sort_and_fill_kernel\(const")
+    kernel = body(text, r"sort_kernel\(const")
     assert 0 <= kernel.find("cluster_arrive()") < kernel.index("sort_cluster(")
     sort = body(text, r"void sort_cluster\(")
     calls = [m.start() for m in re.finditer(r"sort_bases\(", sort)]
