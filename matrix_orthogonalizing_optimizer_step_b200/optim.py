@@ -70,7 +70,7 @@ class MuonHybrid(torch.optim.Optimizer):
     @torch.no_grad()
     def step(self, closure=None):
         loss = closure() if closure is not None else None
-        lanes = {}
+        lanes, counted = {}, []
         for g in self.param_groups:
             ps = [p for p in g["params"] if p.grad is not None]
             if not ps:
@@ -86,6 +86,9 @@ class MuonHybrid(torch.optim.Optimizer):
                 lanes["muon"] = (g, dts, self._muon_lane(ps))
             else:
                 lanes["adamw"] = (g, dts, self._adamw_lane(ps))
+                counted += ps
+        for p in counted:  # nothing above has been refused
+            self.state[p]["step"] += 1
         if "muon" in lanes and "adamw" in lanes and lanes["muon"][1] == lanes["adamw"][1] \
                 and len(lanes["adamw"][2]) == 1:
             # one hybrid call: both lanes in one elementwise launch
@@ -123,8 +126,8 @@ class MuonHybrid(torch.optim.Optimizer):
         return W, G, M
 
     def _adamw_lane(self, ps):
-        """{step count: (params, grads, exp_avg, exp_avg_sq)} after advancing
-        every parameter's step count."""
+        """{step count: (params, grads, exp_avg, exp_avg_sq)} of the step to
+        come; the caller advances the counts once every lane is assembled."""
         by_step = {}
         for p in ps:
             st = self.state[p]
@@ -132,8 +135,7 @@ class MuonHybrid(torch.optim.Optimizer):
                 st["exp_avg"] = torch.zeros(p.numel(), dtype=torch.float32, device=p.device)
                 st["exp_avg_sq"] = torch.zeros(p.numel(), dtype=torch.float32, device=p.device)
                 st["step"] = 0
-            st["step"] += 1
-            lists = by_step.setdefault(st["step"], ([], [], [], []))
+            lists = by_step.setdefault(st["step"] + 1, ([], [], [], []))
             lists[0].append(p.view(-1))
             lists[1].append(self._dense_grad(p).view(-1))
             lists[2].append(st["exp_avg"])
