@@ -153,7 +153,7 @@ class MuonHybrid(torch.optim.Optimizer):
         tokens, rows = g._indices()[0].contiguous(), g._values().contiguous()
         kept = self.__dict__.setdefault("_row_grads", {})
         out = kept.get(p)
-        if out is not None and (out.dtype != rows.dtype or out.shape != p.shape):
+        if out is not None and (out.dtype != rows.dtype or out.shape != p.shape or out.device != rows.device):
             out = None
         kept[p] = muon_embedding_backward(tokens, rows, p.shape[0], out=out)
         return kept[p]

@@ -76,3 +76,14 @@ def test_counts_of_parameters_that_skip_steps(calls):
     emb.grad = row_sparse(emb, [0])
     opt.step()
     assert [c[:2] for c in calls if c[0] == "adamw"] == [("adamw", 1), ("adamw", 1), ("adamw", 2)]
+
+
+def test_buffer_of_row_sparse_gradients_follows_its_parameter(calls):
+    """After model.to(other device) the buffer is a new one there."""
+    _, emb, _ = parameters()
+    opt = optim.MuonHybrid([], [emb])
+    opt._row_grads[emb] = torch.empty(8, 4, device="meta")
+    emb.grad = row_sparse(emb, [1, 2, 1])
+    opt.step()
+    assert opt._row_grads[emb].device == emb.device
+    assert torch.equal(calls[-1][2][0], emb.grad.to_dense().view(-1))
