@@ -19,7 +19,7 @@ gradient and parameter dtypes are set to match.
 An AdamW parameter's gradient may be row-sparse, as torch.nn.Embedding(...,
 sparse=True) leaves it: (token, row) pairs, tokens repeated.  The step sums it
 into a dense gradient with muon_embedding_backward (in a buffer kept per
-parameter) and goes on as with a dense one: moments and weight decay reach
+parameter while its gradients are row-sparse) and goes on as with a dense one: moments and weight decay reach
 every row.
 """
 from __future__ import annotations
@@ -144,14 +144,15 @@ class MuonHybrid(torch.optim.Optimizer):
 
     def _dense_grad(self, p):
         g = p.grad
+        kept = self.__dict__.setdefault("_row_grads", {})
         if not g.is_sparse:
+            kept.pop(p, None)
             return g
         if p.dim() != 2 or g.sparse_dim() != 1:
             raise TypeError("a sparse gradient must hold rows of a 2-D parameter")
         from . import muon_embedding_backward
         # not coalesced: the kernel sums equal tokens itself
         tokens, rows = g._indices()[0].contiguous(), g._values().contiguous()
-        kept = self.__dict__.setdefault("_row_grads", {})
         out = kept.get(p)
         if out is not None and (out.dtype != rows.dtype or out.shape != p.shape or out.device != rows.device):
             out = None

@@ -87,3 +87,16 @@ def test_buffer_of_row_sparse_gradients_follows_its_parameter(calls):
     opt.step()
     assert opt._row_grads[emb].device == emb.device
     assert torch.equal(calls[-1][2][0], emb.grad.to_dense().view(-1))
+
+
+def test_buffer_of_row_sparse_gradients_is_reused_and_dropped(calls):
+    _, emb, _ = parameters()
+    opt = optim.MuonHybrid([], [emb])
+    emb.grad = row_sparse(emb, [1, 2, 1])
+    opt.step()
+    opt.step()
+    first, second = (c[1] for c in calls if c[0] == "embedding_backward")
+    assert first is second
+    emb.grad = torch.randn(8, 4)  # dense from here on: nothing is kept
+    opt.step()
+    assert not opt._row_grads
