@@ -32,6 +32,11 @@ def _rows(g):
     return g.contiguous()
 
 
+def _check_padding(padding_idx, vocab):
+    if padding_idx is not None and not 0 <= padding_idx < vocab:
+        raise ValueError("padding_idx must be a token of the vocabulary (0 or more)")
+
+
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, weight, scale, padding_idx, out_dtype):
@@ -52,6 +57,7 @@ class _Embedding(torch.autograd.Function):
 def embedding(tokens, weight, scale=1.0, padding_idx=None, out_dtype=None):
     """scale * weight[tokens] in out_dtype (default: the weight's).  The
     weight's gradient is dense, in the weight's dtype; padding_idx gets none."""
+    _check_padding(padding_idx, weight.shape[0])
     tokens = tokens.contiguous()
     return _Embedding.apply(tokens, weight, scale, padding_idx, out_dtype)
 
@@ -124,6 +130,7 @@ class Embedding(torch.nn.Module):
 
     def __init__(self, num_embeddings, dim, scale=1.0, padding_idx=None, out_dtype=None, device=None, dtype=None):
         super().__init__()
+        _check_padding(padding_idx, num_embeddings)
         self.scale, self.padding_idx, self.out_dtype = scale, padding_idx, out_dtype
         self.weight = torch.nn.Parameter(torch.empty(num_embeddings, dim, device=device, dtype=dtype))
         torch.nn.init.normal_(self.weight, std=0.02)

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import matrix_orthogonalizing_optimizer_step_b200 as mo
-from matrix_orthogonalizing_optimizer_step_b200 import optim
+from matrix_orthogonalizing_optimizer_step_b200 import layers, optim
 
 
 @pytest.fixture
@@ -100,3 +100,14 @@ def test_buffer_of_row_sparse_gradients_is_reused_and_dropped(calls):
     emb.grad = torch.randn(8, 4)  # dense from here on: nothing is kept
     opt.step()
     assert not opt._row_grads
+
+
+def test_embedding_refuses_a_padding_index_outside_the_vocabulary():
+    """In the forward pass, where torch's own layer would take a negative one,
+    not in the backward pass of a step that has run."""
+    w, t = torch.zeros(5, 8, requires_grad=True), torch.tensor([1, 2])
+    for bad in (-1, 5):
+        with pytest.raises(ValueError, match="padding_idx"):
+            layers.embedding(t, w, padding_idx=bad)
+        with pytest.raises(ValueError, match="padding_idx"):
+            layers.Embedding(5, 8, padding_idx=bad)
