@@ -119,16 +119,17 @@ __device__ __forceinline__ void copy_row(uint32_t slot, const T* p, int dim, int
     }
 }
 
-// Units of this thread as floats, 0 behind the last column.
+// Units of this thread as floats, `none` behind the last column.
 template <typename T, class S>
-__device__ __forceinline__ void read_row(const uint4* slot, const T* p, int dim, int tr, float (&v)[S::NU][S::VL]) {
+__device__ __forceinline__ void read_row(const uint4* slot, const T* p, int dim, int tr, float (&v)[S::NU][S::VL],
+                                         float none = 0.f) {
 #pragma unroll
     for (int u = 0; u < S::NU; ++u) {
         if (S::ACCESS == DIRECT) {
 #pragma unroll
             for (int j = 0; j < S::VL; ++j) {
                 const int c = row_col<S>(u, j, tr);
-                v[u][j] = c < dim ? to_float(p[c]) : 0.f;
+                v[u][j] = c < dim ? to_float(p[c]) : none;
             }
         } else {
             const uint4 raw = slot[u * S::threads];
@@ -141,7 +142,7 @@ __device__ __forceinline__ void read_row(const uint4* slot, const T* p, int dim,
                     f = __uint_as_float(w[j & 3]);
                 else
                     f = __uint_as_float((j & 1) ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
-                v[u][j] = in ? f : 0.f;
+                v[u][j] = in ? f : none;
             }
         }
     }
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(S::threads) norm_grad_kernel(const NormBwd L, 
             copy_wait<kAhead>();
         }
         float xv[S::NU][S::VL], g[S::NU][S::VL];
-        read_row<T, S>(slot(st, 0), x + at * L.ldx, dim, tr, xv);
+        read_row<T, S>(slot(st, 0), x + at * L.ldx, dim, tr, xv, mu);
         read_row<T, S>(slot(st, 1), dy + at * L.ldy, dim, tr, g);
         if (S::stages > 0 && ++st == S::stages) st = 0;
         float s[2] = {0.f, 0.f};
@@ -395,8 +396,8 @@ __global__ void __launch_bounds__(S::threads) norm_grad_kernel(const NormBwd L, 
                 if (!S::keep) load_param<S>(L.w, L.p_dt, dim, tr, u, 1.f, w);
 #pragma unroll
                 for (int j = 0; j < S::VL; ++j) {
-                    // columns behind the last hold x = g = 0 and add nothing that
-                    // is stored; their product in s1 is 0 for any finite statistic
+                    // columns behind the last hold x = mu and g = 0: they add
+                    // nothing, however large mu and r are
                     const float xh = (xv[u][j] - mu) * r;
                     xv[u][j] = xh;
                     aw[u][j] = fmaf(g[u][j], xh, aw[u][j]);

@@ -19,8 +19,8 @@ gradient and parameter dtypes are set to match.
 An AdamW parameter's gradient may be row-sparse, as torch.nn.Embedding(...,
 sparse=True) leaves it: (token, row) pairs, tokens repeated.  The step sums it
 into a dense gradient with muon_embedding_backward (in a buffer kept per
-parameter while its gradients are row-sparse) and goes on as with a dense one: moments and weight decay reach
-every row.
+parameter while its gradients are row-sparse) and goes on as with a dense
+one: moments and weight decay reach every row.
 """
 from __future__ import annotations
 

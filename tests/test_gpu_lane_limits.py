@@ -109,3 +109,23 @@ def test_embedding_backward_zeros_of_large_tables(vocab, dim, offset, n, dtype):
     assert torch.equal(out.double(), integer_sums(t, g, vocab))
     assert (flat[:offset] == 5).all() and (flat[offset + vocab * dim:] == 5).all()
     status_ok()
+
+
+# ---- LayerNorm -----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_layer_norm_backward_of_huge_rows(dtype):
+    """Equal values of 2^125: the row's mean times rstd passes fp32, the
+    differences to the mean are 0.  The places behind the last column, where x
+    counts as nothing, must not add a product of 0 and infinity."""
+    for dim in (2, 4):
+        x = torch.full((3, dim), 2.0 ** 125, device=DEV, dtype=dtype)
+        y, mean, rstd = mo.muon_layer_norm(x)
+        assert (y == 0).all() and (mean == 2.0 ** 125).all() and torch.isinf(mean * rstd).all()
+        dy = torch.randn(3, dim, generator=gen(2), device=DEV).to(dtype)
+        got = mo.muon_layer_norm_backward(dy, x, mean, rstd, torch.ones(dim, device=DEV))
+        want, bound = ref.norm_grad(dy, x, mean, rstd, torch.ones(dim, device=DEV))
+        for a, v, e in zip(got, want, bound):
+            ref.close(a, v, e + ref.half(a.dtype) * (v.abs() + e))
+    status_ok()
