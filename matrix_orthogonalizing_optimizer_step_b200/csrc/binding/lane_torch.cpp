@@ -192,7 +192,7 @@ std::tuple<Tensor, Tensor, Tensor> layer_norm(const Tensor& x, const optional<Te
 
 std::tuple<Tensor, optional<Tensor>, optional<Tensor>> layer_norm_backward(
     const Tensor& grad_out, const Tensor& x, const Tensor& mean, const Tensor& rstd, const optional<Tensor>& weight,
-    bool bias, optional<ScalarType> param_dtype) {
+    bool bias, optional<ScalarType> param_dtype, bool weight_grad) {
     const int xd = dtype_code(x.scalar_type(), "x");
     TORCH_CHECK_VALUE(grad_out.sizes() == x.sizes() && grad_out.scalar_type() == x.scalar_type(),
                       "grad_out must have x's shape and dtype");
@@ -209,7 +209,7 @@ std::tuple<Tensor, optional<Tensor>, optional<Tensor>> layer_norm_backward(
     pd = dtype_code(pt, "param_dtype");
     Tensor dx = empty(x.sizes(), x.scalar_type(), x);
     optional<Tensor> dw, db;
-    if (weight) dw = empty(weight->sizes(), pt, x);
+    if (weight && weight_grad) dw = empty(weight->sizes(), pt, x);
     if (bias) db = empty({r.dim}, pt, x);
     const Tensor ws = workspace(muon_layer_norm_backward_workspace(r.rows, r.dim), x);
     Call call(x);
@@ -300,9 +300,10 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
           "LayerNorm over x's last dimension: (y, mean, rstd).  x bf16 or fp32 with contiguous rows; weight and bias "
           "bf16 or fp32.  y is contiguous in x's dtype; mean and rstd are fp32, one per row, for the backward pass.");
     m.def("muon_layer_norm_backward", &layer_norm_backward, "grad_out"_a, "x"_a, "mean"_a, "rstd"_a,
-          "weight"_a = py::none(), "bias"_a = true, "param_dtype"_a = py::none(),
+          "weight"_a = py::none(), "bias"_a = true, "param_dtype"_a = py::none(), "weight_grad"_a = true,
           "Gradients of muon_layer_norm: (dx, dweight, dbias) in x's dtype and in the weight's (without a weight: "
-          "param_dtype, default fp32).  dweight is None without a weight, dbias None with bias=False.");
+          "param_dtype, default fp32).  dweight is None without a weight or with weight_grad=False, dbias None with "
+          "bias=False.");
     m.def("muon_head_loss", &head_loss, "hidden"_a, "weight"_a, "targets"_a, "ignore_index"_a = -100,
           "(loss, lse) per token of the softmax cross entropy of hidden . weight^T: hidden (..., dim) and weight "
           "(vocab, dim) bf16 with dim a multiple of 8, targets int32 or int64.  Both results are fp32 in targets' "

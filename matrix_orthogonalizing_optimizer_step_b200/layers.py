@@ -74,9 +74,9 @@ class _LayerNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad):
         x, weight, mean, rstd = ctx.saved_tensors
-        dx, dw, db = _mo.muon_layer_norm_backward(_rows(grad), x, mean, rstd, weight,
-                                                  bias=ctx.bias_dtype is not None,
-                                                  param_dtype=ctx.bias_dtype if weight is None else None)
+        dx, dw, db = _mo.muon_layer_norm_backward(_rows(grad), x, mean, rstd, weight, bias=ctx.needs_input_grad[2],
+                                                  param_dtype=ctx.bias_dtype if weight is None else None,
+                                                  weight_grad=ctx.needs_input_grad[1])
         return dx, dw, db, None
 
 

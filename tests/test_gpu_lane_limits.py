@@ -129,3 +129,28 @@ def test_layer_norm_backward_of_huge_rows(dtype):
         for a, v, e in zip(got, want, bound):
             ref.close(a, v, e + ref.half(a.dtype) * (v.abs() + e))
     status_ok()
+
+
+def test_layer_norm_backward_of_frozen_parameters():
+    """Without a parameter to train there is nothing to add up over the rows:
+    one launch.  The gradients that are asked for are the same."""
+    x = torch.randn(50, 96, generator=gen(3), device=DEV)
+    g = torch.randn(50, 96, generator=gen(4), device=DEV)
+
+    def run(*trained):
+        ps = [x.clone(), torch.full((96,), 1.5, device=DEV), torch.zeros(96, device=DEV)]
+        for p, on in zip(ps, trained):
+            p.requires_grad_(on)
+        y = layers.layer_norm(*ps)
+        before = mo.muon_launch_count()
+        y.backward(g)
+        return [p.grad for p in ps], mo.muon_launch_count() - before
+
+    full, launches = run(True, True, True)
+    assert launches == 2
+    for trained in ((True, False, False), (True, True, False), (True, False, True), (False, True, True)):
+        grads, launches = run(*trained)
+        assert launches == (2 if trained[1] or trained[2] else 1), trained
+        for on, got, want in zip(trained, grads, full):
+            assert torch.equal(got, want) if on else got is None
+    status_ok()
