@@ -154,3 +154,63 @@ def test_layer_norm_backward_of_frozen_parameters():
         for on, got, want in zip(trained, grads, full):
             assert torch.equal(got, want) if on else got is None
     status_ok()
+
+
+# ---- output head ---------------------------------------------------------------
+
+
+def rounded_between(got, lo, hi):
+    """got (bf16) is the rounding of a number in [lo, hi] (64 bits), element by element."""
+    got = got.float()
+    return (got >= lo.float().to(BF).float()) & (got <= hi.float().to(BF).float())
+
+
+@pytest.mark.parametrize("n,ignored", [(40, 0.0), (300, 0.3), (900, 0.05)])
+def test_head_loss_targets_entry_of_dhidden(n, ignored):
+    """Row k of the weight is zero but in columns of its own, so those columns
+    of dhidden, in a token whose target is k, are dloss (p - 1) w_k and nothing
+    else: they must be its rounding, without the rounding of P.  p lies between
+    0.1 and 0.4 of a vocabulary of 600, most of it zero rows."""
+    vocab, used, width = 600, 8, 8
+    dim = used * width
+    rows = torch.arange(used, device=DEV) * 73 + 5  # in several 128-column stretches
+    w = torch.zeros(vocab, dim, device=DEV)
+    for k in range(used):
+        w[rows[k], k * width:(k + 1) * width] = torch.randint(8, 16, (width,), generator=gen(20 + k), device=DEV) / 8
+    k = torch.arange(n, device=DEV) % used
+    # the own logit is about log(vocab p / (1 - p)); the others stay near zero
+    p0 = 0.1 + 0.3 * torch.rand(n, generator=gen(30), device=DEV)
+    own = torch.log(600 * p0 / (1 - p0))
+    h = torch.zeros(n, used, width, device=DEV)
+    h[torch.arange(n, device=DEV), k] = (own / w[rows[k]].sum(1))[:, None].expand(n, width)
+    h = h.view(n, dim).to(BF)
+    w = w.to(BF)
+    t = rows[k].clone()
+    dloss = torch.rand(n, generator=gen(31), device=DEV) * 2 - 0.7
+    gone = torch.rand(n, generator=gen(32), device=DEV) < ignored
+    t[gone] = -100
+    h[gone] = float("nan")
+    _, lse = mo.muon_head_loss(h, w, t)
+    dh, _ = mo.muon_head_loss_backward(h, w, t, lse, dloss)
+    _, vlse, p, valid, h64, at = ref.head(h, w, t, -100)
+    assert torch.equal(valid, ~gone)
+    _, blse, bl = ref.head_bounds(h64, w, vlse, valid)
+    i = torch.arange(n, device=DEV)[valid]
+    py, dl, wy = p[i, at[i]], dloss[i].double(), w.double()[at[i]]
+    assert 0.05 < py.min() and py.max() < 0.5
+    # the exponential, the scaling of dloss, the products with dloss and the
+    # difference; then the product with w, the sum with what P's rounding took
+    # off and the scaling back
+    e = dl.abs() * (py * (torch.expm1((bl + blse)[i]) + 2.0 ** -20) + 6 * ref.U)
+    g = dl * (py - 1)
+    want, bound = g[:, None] * wy, e[:, None] * wy.abs() + 4 * ref.U * (g[:, None] * wy).abs()
+    mine = wy != 0
+    inside = rounded_between(dh[i], want - bound, want + bound)
+    assert inside[mine].all()
+    # the check tells a P that was rounded and not mended from one that was
+    # (its factor, the largest |dloss|, is left out of the rounding)
+    top = dl.abs().max()
+    bare = ((g / top).float().to(BF).double() * top)[:, None] * wy
+    assert (~rounded_between(bare.float().to(BF), want - bound, want + bound))[mine].float().mean() > 0.1
+    assert (dh[gone] == 0).all()
+    status_ok()
