@@ -477,12 +477,14 @@ MUON_API int muon_head_loss(const void* hidden, long long ld_hidden, const void*
  * muon_head_loss_backward -- with p = dloss (softmax(l) - onehot(target)):
  *     dhidden = p weight,  dweight = p^T hidden,
  * both bf16, contiguous and 16-byte aligned; either may be NULL (not
- * computed).  lse is the forward call's; dloss (fp32, one per
- * token) is the gradient of the per-token loss.  p is rounded to bf16 for the
- * two products (as the tensor cores take it), whose sums are fp32.  The
- * vocabulary is walked in pieces whose p fits in 512 MiB (one 256-column tile
- * at least).  dhidden is 0 for ignored tokens, and so is their share of
- * dweight whatever their dloss and hidden rows hold.
+ * computed).  lse is the forward call's; dloss (fp32, one per token) is the
+ * gradient of the per-token loss.  p is rounded to bf16 for the two products
+ * (as the tensor cores take it), whose sums are fp32.  A target's own p is made
+ * from the fp32 lse and off by up to about (2^-24 |lse| + 2^-21) dloss: where
+ * the loss itself is smaller than that, the token's gradient is of that size
+ * and has no correct digit.  The vocabulary is walked in pieces whose p fits in
+ * 512 MiB (one 256-column tile at least).  dhidden is 0 for ignored tokens, and
+ * so is their share of dweight whatever their dloss and hidden rows hold.
  */
 MUON_API int muon_head_loss_backward(const void* hidden, long long ld_hidden, const void* weight, const void* targets,
                                      int target_dtype, long long tokens, long long vocab, long long dim,

@@ -95,9 +95,11 @@ static_assert(SMEM_BYTES <= 232448, "over the 227 KB of shared memory a CTA may 
 
 constexpr int PART_COLS = 128;  // columns of one (max, sum) pair
 
-// exp(x) as 2^(x log2 e) on the special function unit (relative error about
-// 2^-22 next to fp32's 2^-24; the products' own error is larger).  Callers
-// pass differences to a row's maximum or log sum, formed before the scaling.
+// exp(x) as 2^(x log2 e) on the special function unit.  The unit's relative
+// error is about 2^-22; the roundings of x log2 e and of the constant add up to
+// |x| 2^-24 and |x| 2^-26: 2^-20 to 2^-19 in all at |x| = 12.  The logits' own error is
+// larger, and P is rounded by up to 2^-8 of its value.  Callers pass differences
+// to a row's maximum or log sum, formed before the scaling.
 __device__ __forceinline__ float exp_diff(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
@@ -561,6 +563,8 @@ __device__ void epilogue_warps(const HeadGemm& L, int nvalid, Shared* sh, uint32
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = dl * exp_diff(v[j] - lse);
                 if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+                    // (lse is one fp32 number: off by up to 2^-24 |lse| dl, which is all
+                    // there is of g where the loss is that small)
                     const float g = dl * exp_diff(ly - lse) - dl;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)

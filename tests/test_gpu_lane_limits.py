@@ -214,3 +214,45 @@ def test_head_loss_targets_entry_of_dhidden(n, ignored):
     assert (~rounded_between(bare.float().to(BF), want - bound, want + bound))[mine].float().mean() > 0.1
     assert (dh[gone] == 0).all()
     status_ok()
+
+
+def test_head_loss_gradients_of_confident_rows():
+    """Rows whose target leads by 8 to 40.  The target's entry of P is
+    dloss (exp(l - lse) - 1) with l the same number in both passes, so that l's
+    own error cancels and the entry is off by half a step of lse, by the
+    exponential's error next to 1 and by the sum's, however small the loss is.
+    Every other entry is off relative to itself."""
+    n, vocab, dim = 300, 5003, 2048
+    w = (torch.randn(vocab, dim, generator=gen(97), device=DEV) * 0.02).to(BF)
+    t = torch.randint(0, vocab, (n,), generator=gen(98), device=DEV)
+    lead = torch.linspace(8, 40, n, device=DEV)[:, None]
+    wt = w[t].float()
+    h = (torch.randn(n, dim, generator=gen(99), device=DEV) * 0.1 + wt * (lead / wt.square().sum(1, keepdim=True))).to(BF)
+    dloss = torch.rand(n, generator=gen(100), device=DEV) + 0.5
+    _, lse = mo.muon_head_loss(h, w, t)
+    dh, dw = mo.muon_head_loss_backward(h, w, t, lse, dloss)
+    _, vlse, p, valid, h64, at = ref.head(h, w, t, -100)
+    _, _, el = ref.head_bounds(h64, w, vlse, valid)
+    i, w64, dl = torch.arange(n, device=DEV), w.double(), dloss.double()[:, None]
+    g = p.clone()
+    g[i, at] = 0
+    rest = g.sum(1, keepdim=True)  # 1 - p of the target with all its digits
+    # another entry: two logits' errors, the exponential (2^-22 and |x| steps
+    # of its argument, |x| < 64), dloss
+    rel = torch.expm1(2 * el)[:, None] + 2.0 ** -22 + 70 * ref.U
+    e = dl * g * rel
+    # the target's: the others' sum, the additions to the sum that holds its 1
+    # (128 columns, the pairs of a group, 32 groups), lse's half step and log,
+    # the exponential next to 1, dloss and the difference
+    additions = 128 + 2 * (vocab / 4096 + 1) + 2 * 32
+    e[i, at] = (dl * (rest * rel + additions * ref.U + ref.U * vlse.abs()[:, None] + 2.0 ** -22 + 4 * ref.U))[:, 0]
+    g[i, at] = -rest[:, 0]
+    g = g * dl
+    # P as the products take it, and their sums
+    e = e + ref.half(BF) * (g.abs() + e)
+    dh64, dw64 = g @ w64, g.T @ h64
+    edh = e @ w64.abs() + vocab * 2.0 ** -23 * (g.abs() @ w64.abs())
+    edw = e.T @ h64.abs() + n * 2.0 ** -23 * (g.abs().T @ h64.abs())
+    ref.close(dh, dh64, edh + ref.half(BF) * (dh64.abs() + edh))
+    ref.close(dw, dw64, edw + ref.half(BF) * (dw64.abs() + edw))
+    status_ok()
