@@ -111,6 +111,41 @@ def test_embedding_backward_zeros_of_large_tables(vocab, dim, offset, n, dtype):
     status_ok()
 
 
+@pytest.mark.parametrize("n", [300, 20_000])
+def test_embedding_backward_of_large_tables_in_graphs_and_streams(n):
+    """The three launches of a large table's gradient (by classes and by sorting),
+    captured twice and replayed on two streams at once, over tables that hold
+    something else before."""
+    vocab, dim = 130_001, 24
+    sets = []
+    for seed in (9, 10):
+        g = torch.randint(-3, 4, (n, dim), generator=gen(seed), device=DEV).float()
+        t = torch.randint(0, vocab, (n,), generator=gen(seed + 10), device=DEV)
+        out = torch.empty(vocab, dim, device=DEV)
+        mo.muon_embedding_backward(t, g, vocab, out=out)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            mo.muon_embedding_backward(t, g, vocab, out=out)
+        sets.append((t, g, out, graph, torch.cuda.Stream()))
+    for repeat in range(3):
+        for t, g, out, graph, stream in sets:
+            stream.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(stream):
+                out.fill_(7)
+                graph.replay()
+                t.copy_(t.roll(1))  # after the call has read them
+        torch.cuda.synchronize()
+        for t, g, out, _, _ in sets:
+            assert torch.equal(out.double(), integer_sums(t.roll(-1), g, vocab)), repeat
+    # eager calls behind one another: each starts after the one before has ended
+    for t, g, out, _, _ in sets:
+        got = [mo.muon_embedding_backward(q, g, vocab, out=out).clone() for q in (t, t.flip(0), t // 2)]
+        for a, q in zip(got, (t, t.flip(0), t // 2)):
+            assert torch.equal(a.double(), integer_sums(q, g, vocab))
+    status_ok()
+
+
 # ---- LayerNorm -----------------------------------------------------------------
 
 
