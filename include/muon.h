@@ -396,8 +396,9 @@ MUON_API int muon_normalize_noalloc(int batch, int m, int n, const void* X, void
  *    device, as must every pointer.  Sums and statistics are fp32 and each
  *    output is rounded once.  Results repeat bit for bit.
  *  - `workspace` is the caller's: 256-byte aligned, at least the bytes that the
- *    matching *_workspace function returns (host only; < 0 on an argument
- *    error), with any contents, used until the call's work has ended.  Calls
+ *    matching *_workspace function returns for the call's own sizes (host only;
+ *    < 0 on an argument error; muon_head_loss_backward may need more for fewer
+ *    tokens), with any contents, used until the call's work has ended.  Calls
  *    may be captured into a CUDA graph; graphs and streams that may run at the
  *    same time need workspaces of their own.  The first call on a device
  *    allocates the status word and is refused under capture.

@@ -57,3 +57,14 @@ def test_rows_near_the_most_tokens_stay_in_range():
     kernel = body(source("head_loss.cu"), r"head_rows_kernel\(const")
     assert "t1 = rows_end(blockIdx.x, per, A.tokens)" in kernel
     assert re.search(r"for \(unsigned r = all \+ ", kernel)
+
+
+def test_workspaces_for_more_tokens_do_for_fewer():
+    """A program may size a workspace once, for its longest batch."""
+    lib = mo.lib()
+    counts = [*range(0, 70), 1000, 4095, 4096, 4097, 4100, 5000, 8191, 8192, 8193, 16383, 16384, 16385, 100_000]
+    for dim in (1, 8, 256, 333, 4096):
+        sizes = [lib.muon_embedding_backward_workspace(n, 1000, dim) for n in counts]
+        assert sizes == sorted(sizes)
+        sizes = [lib.muon_layer_norm_backward_workspace(n, dim) for n in counts]
+        assert sizes == sorted(sizes)
