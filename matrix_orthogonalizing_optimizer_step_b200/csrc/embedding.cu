@@ -106,12 +106,13 @@ __global__ void __launch_bounds__(kFwdWarps * 32) embedding_kernel(const EmbedFw
 // ---- gradient: order of up to kClassTokens tokens by classes of the vocabulary -----
 
 // Ordered positions of a reduction chunk.  A short batch is a chain of latencies
-// and a chunk of 8 is one trip to memory less; a long one has more runs that cross
-// chunks of 8 (300 tokens of 20000 x 768 fp32 16.5 instead of 18.8 us with 16, 2000
-// of 40000 x 512 bf16 16.9 instead of 18.6; 8192 of 50257 x 768 27.7 instead of 26.6,
-// 32768 62 instead of 52).
+// and a chunk of 8 is one trip to memory less (300 tokens of 20000 x 768 fp32 16.5
+// instead of 18.8 us with 16); in a longer one more runs cross chunks of 8, and
+// their partial rows are added one after another (512 tokens, half of them equal,
+// 768 wide 19.5 instead of 16.3, 2000 29.6 instead of 22.8; 32768 of 50257 x 768 62
+// instead of 52).
 constexpr int kLongChunk = 16, kShortChunk = 8;
-constexpr long long kShortCount = 4096;
+constexpr long long kShortCount = 384;
 __host__ __device__ constexpr int chunk_of(long long count) { return count <= kShortCount ? kShortChunk : kLongChunk; }
 constexpr int kClassTokens = 16384;
 constexpr int kClassRows = 2048;          // table rows of a class at most
@@ -267,20 +268,27 @@ __global__ void __launch_bounds__(kClassThreads) class_group_kernel(const ClassA
     for (int w = 0; w < lists; ++w) {
         const int k = lists == 1 ? total : warp_n[w];
         const unsigned* l = list + w * items * 32;
-        for (int i0 = 0; i0 < k; i0 += 32) {
-            const unsigned e = i0 + lane < k ? l[i0 + lane] : 0, r = e >> kPosBits;
-            const bool on = i0 + lane < k && r % kClassWarps == warp;
-            if (!__any_sync(0xffffffffu, on)) continue;
-            const unsigned peers = __match_any_sync(0xffffffffu, on ? r : ~0u);
-            unsigned at = 0;
-            if (on) {
-                at = start[r] + __popc(peers & ((1u << lane) - 1));
-                A.keys[before + at] = cls + r * classes;
-                A.pos[before + at] = e & ((1u << kPosBits) - 1);
+        constexpr int kAhead = 4;
+        for (int i0 = 0; i0 < k; i0 += kAhead * 32) {
+            unsigned e[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) e[i] = i0 + i * 32 + lane < k ? l[i0 + i * 32 + lane] : 0;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const unsigned r = e[i] >> kPosBits;
+                const bool on = i0 + i * 32 + lane < k && r % kClassWarps == warp;
+                if (!__any_sync(0xffffffffu, on)) continue;
+                const unsigned peers = __match_any_sync(0xffffffffu, on ? r : ~0u);
+                unsigned at = 0;
+                if (on) {
+                    at = start[r] + __popc(peers & ((1u << lane) - 1));
+                    A.keys[before + at] = cls + r * classes;
+                    A.pos[before + at] = e[i] & ((1u << kPosBits) - 1);
+                }
+                __syncwarp();
+                if (on && (peers >> lane) == 1u) start[r] = static_cast<unsigned short>(at + 1);  // the last of them
+                __syncwarp();
             }
-            __syncwarp();
-            if (on && (peers >> lane) == 1u) start[r] = static_cast<unsigned short>(at + 1);  // the last of them
-            __syncwarp();
         }
     }
     if (cls == classes - 1)  // tokens that take no part
@@ -542,8 +550,8 @@ constexpr int kRunWarps = 4;
 // Chunks behind `chunk` (up) or before it (down) that the run of `key` reaches
 // into: up, the later chunks that start with it, down, the earlier ones that
 // end with it (whole warp).  Equal keys lie together, so a chunk that the run
-// does not reach ends it: one look at the 32 nearest chunks, then at doubling
-// distances, then at 32 places between the last hit and the first miss until
+// does not reach ends it: two looks at the 32 nearest and the next chunks, one at
+// doubling distances, then at 32 places between the last hit and the first miss until
 // they meet.  A run of m chunks costs each of them log m looks (2^21 equal
 // tokens, 8 wide: 6.7 ms, almost all of it the joining warp's; with looks at 32
 // chunks at a time to the run's end 56 ms).
@@ -556,9 +564,11 @@ __device__ __forceinline__ unsigned chunks_of_run(const RunArgs& R, unsigned chu
     };
     unsigned miss = misses(lane + 1);
     if (miss) return __ffs(miss) - 1;
-    miss = misses(64ull << lane);  // (behind the last chunk from the 27th lane on at the latest)
+    miss = misses(lane + 33);
+    if (miss) return __ffs(miss) + 31;
+    miss = misses(128ull << lane);  // (behind the last chunk from the 26th lane on at the latest)
     const int first = __ffs(miss) - 1;
-    unsigned long long hit = 32ull << first, end = 64ull << first;  // the run reaches `hit` chunks, not `end`
+    unsigned long long hit = 64ull << first, end = 128ull << first;  // the run reaches `hit` chunks, not `end`
     while (end - hit > 1) {
         const unsigned long long step = (end - hit + 31) / 32;
         const unsigned long long k = min(hit + step * (lane + 1), end);
