@@ -16,8 +16,8 @@
 //   2. zeros are written over the table, beside the first launch, by one of
 //      their own; where a large part of the rows is asked for, or the table is
 //      small, by the classes' CTAs after their grouping, over the other rows.
-//   3. the order is cut into chunks of 16 positions; a warp sums the rows of
-//      one chunk for 256 columns.  A token whose run lies inside a chunk is
+//   3. the order is cut into chunks of 16 positions (8 in short batches); a warp
+//      sums the rows of one chunk for 256 columns.  A token whose run lies inside a chunk is
 //      written at once.  A run that crosses chunk borders leaves one fp32
 //      partial row per chunk, and the warp that finishes the last of the run's
 //      chunks adds them in order.
@@ -30,11 +30,12 @@
 //
 // Sums are fp32 and rounded once to the gradient's type.
 //
-// Measured (bf16): lookup of 16384 tokens from 128256 x 4096 35 us, 134 MB
-// written and up to as much read (the repeats come from L2); 16 tokens 1.9 us
-// on the GPU.  Gradient of 8192 tokens of 50257 x 768 30.8 us (13.9 us at the
-// copy rate), of 16384 of 128256 x 4096 215 us (183), of 1237 of 5003 x 333
-// fp32 15.3 us.
+// Measured (bf16, calls behind one another on changing inputs): lookup of 16384
+// tokens from 128256 x 4096 35 us, 134 MB written and up to as much read (the
+// repeats come from L2); 16 tokens 1.6 us replayed from a graph.  Gradient of
+// 8192 tokens of 50257 x 768 28 us (13.9 us at the copy rate; 23.4 from a
+// graph), of 16384 of 128256 x 4096 187 us (183), of 1237 of 5003 x 333 fp32
+// 14.3-15.3 us (12.6 from a graph).
 #include <algorithm>
 
 #include "lane.h"
@@ -159,9 +160,10 @@ __device__ __forceinline__ void zero_row(TO* row, long long dim, int lane) {
 
 // CTA c owns the table rows c, c + classes, c + 2 classes, ...: it finds the
 // tokens of its class among all (each CTA reads all of them, from L2) and
-// groups them by row in the order of their positions.  Then, where no launch of
-// its own does it, it writes zeros over the rows that no token asks for.  The order is ready after 4 us (8192
-// tokens), where the sort's two passes take 20: no step of it leaves the CTA.
+// groups them by row in the order of their positions.  Then, where the zeros
+// have no launch of their own, it writes them over the rows that no token asks
+// for.  The order is ready after 4 us (8192 tokens; 10 beside the zeros' launch),
+// where the sort's two passes take 20: no step of it leaves the CTA.
 template <typename TO>
 __global__ void __launch_bounds__(kClassThreads) class_group_kernel(const ClassArgs A) {
     extern __shared__ unsigned class_smem[];
@@ -262,9 +264,9 @@ __global__ void __launch_bounds__(kClassThreads) class_group_kernel(const ClassA
     }
     __syncthreads();
     // A warp groups the rows r = warp, warp + 16, ... in one pass over the list: a
-    // token's place is its row's next one, the row's first lanes first.  (A pass
-    // per row took 5.9 ms where 16384 tokens in 2000 rows were all of one class,
-    // 135 us now, and as long as this where they are spread.)
+    // token's place is its row's next one, the row's first lanes first.  (16384
+    // tokens in 2000 rows, all of one class: 122 us for the call, with a pass per
+    // row 5.9 ms; spread over the classes 33.)
     for (int w = 0; w < lists; ++w) {
         const int k = lists == 1 ? total : warp_n[w];
         const unsigned* l = list + w * items * 32;
@@ -508,9 +510,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
 
 // Zeros over the whole table, beside the launch that orders the tokens, which
 // is its predecessor: whole 16-byte units from the first aligned address on.
-// Short CTAs in the order of the addresses write 7.5 TB/s, as much as a memset;
-// persistent ones, which drift apart, 6.3 in any pattern (2.1 GB: 280 and 330-340
-// us; 16-byte, 32-byte and bulk stores and cache hints alike).
+// Short CTAs in the order of the addresses write 7.5 TB/s, a little more than a
+// memset; persistent ones, which drift apart, 6.3 in any pattern (2.1 GB: 280 and
+// 330-340 us; 16-byte, 32-byte and bulk stores and cache hints alike).
 constexpr int kZeroThreads = 256;
 constexpr int kZeroUnits = 4;
 constexpr long long kZeroBytes = 16ll * kZeroThreads * kZeroUnits;  // of a CTA
@@ -550,11 +552,11 @@ constexpr int kRunWarps = 4;
 // Chunks behind `chunk` (up) or before it (down) that the run of `key` reaches
 // into: up, the later chunks that start with it, down, the earlier ones that
 // end with it (whole warp).  Equal keys lie together, so a chunk that the run
-// does not reach ends it: two looks at the 32 nearest and the next chunks, one at
-// doubling distances, then at 32 places between the last hit and the first miss until
-// they meet.  A run of m chunks costs each of them log m looks (2^21 equal
-// tokens, 8 wide: 6.7 ms, almost all of it the joining warp's; with looks at 32
-// chunks at a time to the run's end 56 ms).
+// does not reach ends it: two looks at the 32 nearest and the next 32 chunks, one
+// at doubling distances, then at 32 places between the last hit and the first
+// miss until they meet.  A run of m chunks costs each of them log m looks (2^21
+// equal tokens, 8 wide: 6.7 ms, almost all of it the joining warp's; with looks
+// at 32 chunks at a time to the run's end 56 ms).
 template <int kChunk>
 __device__ __forceinline__ unsigned chunks_of_run(const RunArgs& R, unsigned chunk, unsigned key, bool up, int lane) {
     auto misses = [&](unsigned long long k) {  // lanes whose chunk, k away, the run does not reach
@@ -580,8 +582,8 @@ __device__ __forceinline__ unsigned chunks_of_run(const RunArgs& R, unsigned chu
 }
 
 // A warp adds the rows of one chunk for 256 columns: items of equal size with
-// 8 rows' loads in flight each (12 us for 8192 x 768, 47 us for 16384 x 4096 with
-// the zeros' last lines still on their way to memory; units of one token's
+// 8 rows' loads in flight each (10-13 us for 8192 x 768, 50 us for 16384 x 4096
+// with the zeros' last lines still on their way to memory; units of one token's
 // rows, of unequal size, took 18 and 75-110 us).  A run inside the chunk is
 // written at once.  A run that crosses the chunk's borders leaves a partial
 // row; the warp that finishes the last of the run's chunks for these columns
@@ -869,13 +871,13 @@ cudaError_t launch_embedding_backward(const EmbedBwd& L, int num_sms, cudaStream
     const int classes = static_cast<int>(std::min<long long>(std::min(num_sms, kMostClasses), L.vocab));
     const bool by_class = L.count > 0 && L.count <= kClassTokens && L.vocab <= kClassVocab &&
                           (L.vocab + classes - 1) / classes <= kClassRows;
-    // The zeros' own launch writes 7.5 TB/s from the first microsecond on and the
+    // The zeros' own launch writes 7.5 TB/s from the first microseconds on and the
     // rows that tokens ask for twice, the classes' CTAs 6.3 TB/s of the others
-    // after 4-10 us of ordering: even where a sixth of the rows is asked for.  (8192
-    // tokens of 50257 x 768 bf16 22.8-26.6 instead of 24.1-28.6 us, 16384 of 128256 x
-    // 4096 190 instead of 203-212, 300 of 128256 x 2001 fp32 147 instead of 194.)  A
-    // launch more costs as much as it gains below 8 MiB (300 of 2500 x 768 fp32: 10.4
-    // and 10.3).
+    // after the ordering: even where a sixth of the rows is asked for.  (One input
+    // set in a loop, distinct to language-like tokens: 8192 of 50257 x 768 bf16
+    // 22.8-26.6 instead of 24.1-28.6 us, 16384 of 128256 x 4096 190 instead of 203-212,
+    // 300 of 128256 x 2001 fp32 147-149 instead of 194-197.)  A launch more costs as
+    // much as it gains below 8 MiB (300 of 2500 x 768 fp32: 10.4 and 10.3).
     constexpr long long kZeroApart = 8ll << 20;
     const bool zero_apart = !by_class || (L.vocab * L.dim * dtype_size(L.out_dt) >= kZeroApart && L.count * 6 <= L.vocab);
     int side = 0;

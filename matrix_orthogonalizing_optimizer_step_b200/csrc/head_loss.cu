@@ -50,10 +50,11 @@
 // Ending the sums every 768 elements and adding the parts in registers gave
 // 7e-7 at 4096 and cost 9-14 % of the forward product.
 //
-// Measured: loss and gradients of 8192 tokens, 50257 x 768, 2.05-2.19 ms (2.53
-// TFLOP: 1.2 PFLOP/s); 3/4 of 4096 tokens, 128256 x 4096, 9.5-9.8 ms (12.9 TFLOP:
-// 1.32-1.37 PFLOP/s under the power cap, where a plain bf16 product sustains
-// 1.43); 61 tokens, 5003 x 256, forward 14.4 us.
+// Measured (calls behind one another on changing inputs): loss and gradients of
+// 8192 tokens, 50257 x 768, 2.18-2.20 ms (2.53 TFLOP: 1.15 PFLOP/s); 3/4 of 4096
+// tokens, 128256 x 4096, 9.73-9.81 ms (12.9 TFLOP: 1.32 PFLOP/s under the power
+// cap, where a plain bf16 product sustains 1.43); 61 tokens, 5003 x 256, forward
+// 14.3 us (11.0 replayed from a graph).
 //
 // Every wait is bounded; on expiry the kernel records a timeout in the device
 // status word, drains its copies and MMAs, frees tensor memory and exits.

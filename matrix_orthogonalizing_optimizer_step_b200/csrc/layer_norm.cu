@@ -21,11 +21,12 @@
 //
 // Statistics and sums are fp32; outputs are rounded once.
 //
-// Measured (bf16): forward 16384 x 4096 48-51 us (268 MB: 5.2-5.6 TB/s), 16 x 4096
-// 2.7 us on the GPU; backward 16384 x 768 with fp32 parameters 18.5 us (75 MB,
-// 11.7 us at the copy rate: rows' chains of latencies and the second launch),
-// 4099 x 1025 fp32 18.5 us (50 MB, 7.8 us: 4-byte copies, and a third of the
-// rows' 1536 places empty).
+// Measured (bf16; calls behind one another on changing inputs, in brackets
+// replayed from a graph on one input, which L2 then holds): forward 16384 x 4096
+// 52 us (46: 268 MB, 5.2-5.8 TB/s), 16 x 4096 6.5 us (2.5); backward 16384 x 768 with
+// fp32 parameters 20.5 us (15.5; 75 MB, 11.7 us at the copy rate: rows' chains of
+// latencies and the second launch), 4099 x 1025 fp32 19.3 us (16.4; 50 MB, 7.8 us:
+// 4-byte copies, and a third of the rows' 1536 places empty).
 #include <atomic>
 
 #include "lane.h"
@@ -71,7 +72,7 @@ struct RowShape {
     static constexpr int stage_bytes = ARRAYS * NU * threads * 16;
     // rows in flight per row group, in about 48 KB per CTA: up to 3 forward
     // (16384 x 4096 bf16: 47.5 us; 2: 49.9, 4: 49.0), 2 backward, where the
-    // registers hold more (16384 x 768: 19.0 us; 3 and 4: 20.5)
+    // registers hold more (16384 x 768, two inputs in a loop: 19.0 us; 3 and 4: 20.5)
     static constexpr int fit = 49152 / stage_bytes, most = ARRAYS == 1 ? 3 : 2;
     static constexpr int stages = ACCESS == DIRECT ? 0 : (fit > most ? most : (fit < 2 ? 2 : fit));
     // the ring, or the sums of a backward CTA's row groups
@@ -565,7 +566,8 @@ __global__ void __launch_bounds__(kSumWarps * 32)
         // two CTAs' rows per SM in one trip to L2; the addresses are stepped, since a
         // kernel this short waits for its own code (a product per load: 18.8 and
         // 17.1 instead of 16.2 us for the whole backward pass of 4099 x 1025 and
-        // 16384 x 768; eight loads at a time with a remainder loop 17.1 and 17.3)
+        // 16384 x 768 replayed from a graph; eight loads at a time with a remainder
+        // loop 17.1 and 17.3)
         constexpr int kAhead = 10;
 #pragma unroll 1
         for (int left = nparts - warp; left > 0; left -= kAhead * kSumWarps) {
